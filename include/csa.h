@@ -253,6 +253,128 @@ csa_status csa_sparse_attn(const csa_attn_args* a, void* workspace, size_t works
                            csa_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Residual addition and root-mean-square norm of token rows, with an output
+ * in the rows' type and / or in E4M3 (the operand of an 8-bit projection).
+ * Row r, channel d (all arithmetic in fp32):
+ *   s      = x + residual                    (x without a residual)
+ *   y      = s * rsqrt(mean_d(s^2) + eps) * weight
+ *   residual_out = s, out = y                (rounded to the rows' type)
+ *   codes, scales by scale_kind:
+ *     CSA_SCALE_NONE    : code = E4M3_rne_sat(y), no scales
+ *     CSA_SCALE_UE8M0X32: per 32 channels the exponent byte e + 127 with e
+ *                         the smallest integer with amax <= 448 * 2^e,
+ *                         clamped to [-127, 127]; code = E4M3_rne_sat(y * 2^-e)
+ *     CSA_SCALE_F32X128 : per 128 channels the fp32 scale amax / 448;
+ *                         code = E4M3_rne_sat(y * (1 / scale)); a zero scale
+ *                         gives zero codes
+ * y enters the codes unrounded.  x, residual, residual_out and out share one
+ * type; residual_out and out may be x or residual themselves (same pointer
+ * and stride), any other overlap is outside the contract.  Non-finite inputs
+ * are outside the contract. */
+typedef enum { CSA_SCALE_NONE = 0, CSA_SCALE_UE8M0X32 = 1, CSA_SCALE_F32X128 = 2 } csa_scale_kind;
+
+typedef struct {
+  int64_t n_rows;            /* >= 0 (0: nothing is done) */
+  int32_t dim;               /* a multiple of 16 in [16, 16384]; of 32 or 128
+                                with CSA_SCALE_UE8M0X32 / CSA_SCALE_F32X128 */
+  int32_t dtype;             /* csa_src_dtype of x, residual, residual_out, out */
+  const void* x;             /* row r at x + r * x_stride elements */
+  int64_t x_stride;          /* elements, >= dim, a multiple of 16 bytes (as every stride) */
+  const void* residual;      /* optional */
+  int64_t residual_stride;
+  void* residual_out;        /* optional (with residual) */
+  int64_t residual_out_stride;
+  const float* weight;       /* optional fp32 [dim] (1 without it) */
+  float eps;                 /* >= 0 */
+  int32_t scale_kind;        /* csa_scale_kind, used with codes */
+  void* out;                 /* optional; out or codes must be given */
+  int64_t out_stride;
+  uint8_t* codes;            /* optional E4M3 [n_rows][dim], row stride in bytes */
+  int64_t codes_stride;
+  void* scales;              /* uint8 or fp32 [n_rows][dim / block] */
+  int64_t scales_stride;     /* elements (no alignment rule) */
+} csa_norm_args;
+
+csa_status csa_rms_norm(const csa_norm_args* a, csa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* A paged latent cache and a batch of sequences on it.  Position p of
+ * sequence b is entry p % page_size of page block_table[b][p / page_size].
+ * The step's new tokens are packed rows: sequence b owns rows
+ * [cu_q[b], cu_q[b + 1]), n_b of them, at positions kv_len[b] - n_b ..
+ * kv_len[b] - 1 (kv_len counts the new tokens).  n_b = 0 is allowed.
+ *   - cu_q, kv_len and block_table are read on the device, so a captured
+ *     graph follows their values.  cu_q starts at >= 0 and does not decrease.
+ *   - Rows from cu_q[B] on (padding of a batch) are neither read nor written.
+ *   - A position without a page (p / page_size >= max_pages, or a table value
+ *     outside [0, n_pages)) holds no entry: nothing is written there, and
+ *     attention leaves it out. */
+typedef struct {
+  uint8_t* pages;            /* entry e of page g at pages + g*page_stride + e*row_stride */
+  int32_t fmt;               /* CSA_FMT_FP4_E2M1_E4M3X16 or CSA_FMT_FP8_E4M3_UE8M0X32 */
+  int32_t page_size;         /* entries per page, 1..65536 (any value) */
+  int64_t n_pages;           /* 1 <= n_pages < 2^31 */
+  int64_t row_stride;        /* bytes, >= 288 / 528, a multiple of 16 */
+  int64_t page_stride;       /* bytes, a multiple of 16 */
+  const int32_t* block_table;  /* [B][max_pages], row b at block_table + b * table_stride */
+  int64_t table_stride;      /* elements, >= max_pages */
+  int32_t max_pages;         /* 1 <= max_pages, max_pages * page_size < 2^31 */
+  int32_t B;                 /* sequences, 1..65536 */
+  const int32_t* cu_q;       /* [B + 1] */
+  const int32_t* kv_len;     /* [B] */
+} csa_paged_kv;
+
+/* Append new latents to the cache: row i of src (512 channels), RMS-normed
+ * with `norm` (y = x * rsqrt(mean(x^2) + eps) * weight, fp32), rotated with
+ * `rope_cs` (channels (448 + 2j, 449 + 2j) times e^{i angle j} of the row's
+ * position), encoded as kv.fmt and written to its position's entry.  Without
+ * norm and rope_cs the entries are bit for bit those of csa_quant_kv.  No two
+ * rows of a call may share an entry. */
+typedef struct {
+  csa_paged_kv kv;
+  const void* src;           /* fp32 / bf16, row i at src + i * src_row_stride elements */
+  int32_t src_dtype;         /* csa_src_dtype */
+  int32_t norm;              /* 1: RMS norm first */
+  int64_t n_rows;            /* rows of src, >= cu_q[B] */
+  int64_t src_row_stride;    /* elements, >= 512, a multiple of 16 bytes */
+  const float* weight;       /* optional fp32 [512] (with norm) */
+  const float* rope_cs;      /* optional fp32 [n_rows][32][2] (cos, sin) */
+  float eps;                 /* >= 0 (with norm) */
+} csa_paged_append_args;
+
+csa_status csa_paged_append(const csa_paged_append_args* a, csa_stream_t stream);
+
+/* MLA attention of each sequence's new tokens over its paged cache (keys =
+ * values = the 512-wide latent, one latent head for every query head).  Row i
+ * of sequence b at position p = kv_len[b] - n_b + (i - cu_q[b]), head h, sees
+ * the entries of positions [0, p], with `window` only (p - window, p]:
+ *   l_e = softmax_scale * <q[i,h], x_e>
+ *   out = sum_e softmax(l, sink_h)_e * x_e ;  lse = log(sum_e exp(l_e) [+ exp(sink_h)])
+ * A row that sees no entry gets out = 0 and lse = sink_h (-inf without a
+ * sink).  One new token per sequence is the decode step, kv_len[b] = n_b a
+ * whole prompt, anything between a chunk; sequences of a call may differ.
+ * Entries must decode to |x| < 65504 and queries hold |q| < 65504 (fp16
+ * operands, fp32 accumulation); rotated queries are rounded to fp16. */
+typedef struct {
+  csa_paged_kv kv;
+  const void* q;             /* bf16, row i head h at q + i*q_row_stride + h*q_head_stride elements */
+  int64_t n_rows;            /* rows of q and out, >= cu_q[B]; n_rows * H < 2^31 */
+  int64_t q_row_stride;      /* elements, multiples of 8 */
+  int64_t q_head_stride;     /* elements, >= 512, a multiple of 8 */
+  int32_t H, D;              /* H in 1..128; D must be 512 */
+  float softmax_scale;       /* >= 0, finite */
+  int32_t window;            /* 0: no window; else >= 1 */
+  const float* sink;         /* optional fp32 [H] sink logits */
+  const float* rope_cs;      /* optional fp32 [n_rows][32][2]: q rotated forward, out back */
+  void* out;                 /* bf16 [n_rows][H][512], contiguous */
+  float* lse;                /* optional fp32 [n_rows][H] (natural log) */
+} csa_paged_attn_args;
+
+size_t csa_paged_attn_workspace_size(const csa_paged_attn_args* a);
+csa_status csa_paged_attn(const csa_paged_attn_args* a, void* workspace, size_t workspace_bytes,
+                          csa_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* A stack of layers, one decode (or prefill) step.
  *   FULL    : encode `append` rows, index.* scoring + Top-K (+ pool build),
  *             then attention with attn.idx = index.idx.

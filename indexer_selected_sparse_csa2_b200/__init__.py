@@ -10,6 +10,9 @@ The entry points mirror ``include/csa.h``:
 * ``csa_index_topk``     - lightning-indexer scores + Top-K (+ candidate pool)
 * ``csa_topk_scores``    - Top-K of given fp32 scores
 * ``csa_sparse_attn``    - sparse MLA attention over selected entries + window
+* ``csa_rms_norm``       - residual addition + RMS norm, with 8-bit output
+* ``csa_paged_append``   - norm, RoPE and encoding of new latents into a paged cache
+* ``csa_paged_attn``     - MLA attention of chunks of new tokens over a paged cache
 * ``csa_layer_step``     - a Full / Reindex / Reuse layer stack
 """
 from __future__ import annotations
@@ -35,6 +38,7 @@ CSA_SRC_F32, CSA_SRC_BF16 = 0, 1
 CSA_FMT_FP4_E2M1_E4M3X16, CSA_FMT_FP8_E4M3_UE8M0X32, CSA_FMT_FP8_E4M3_PLAIN = 0, 1, 2
 CSA_MODE_FULL, CSA_MODE_REINDEX, CSA_MODE_REUSE, CSA_MODE_SWA = 0, 1, 2, 3
 CSA_KEY_E4M3, CSA_KEY_MXFP4 = 0, 1
+CSA_SCALE_NONE, CSA_SCALE_UE8M0X32, CSA_SCALE_F32X128 = 0, 1, 2
 FP4_ENTRY_BYTES, FP8_ENTRY_BYTES = 288, 528
 
 _p = ctypes.c_void_p
@@ -71,6 +75,30 @@ class QuantJob(ctypes.Structure):
 class LayerDesc(ctypes.Structure):
     _fields_ = [("mode", _i32), ("reuse_from", _i32), ("pool_from", _i32),
                 ("append", QuantJob * 3), ("index", IndexArgs), ("attn", AttnArgs)]
+
+
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [("n_rows", _i64), ("dim", _i32), ("dtype", _i32), ("x", _p), ("x_stride", _i64),
+                ("residual", _p), ("residual_stride", _i64), ("residual_out", _p), ("residual_out_stride", _i64),
+                ("weight", _p), ("eps", _f32), ("scale_kind", _i32), ("out", _p), ("out_stride", _i64),
+                ("codes", _p), ("codes_stride", _i64), ("scales", _p), ("scales_stride", _i64)]
+
+
+class PagedKv(ctypes.Structure):
+    _fields_ = [("pages", _p), ("fmt", _i32), ("page_size", _i32), ("n_pages", _i64), ("row_stride", _i64),
+                ("page_stride", _i64), ("block_table", _p), ("table_stride", _i64), ("max_pages", _i32), ("B", _i32),
+                ("cu_q", _p), ("kv_len", _p)]
+
+
+class PagedAppendArgs(ctypes.Structure):
+    _fields_ = [("kv", PagedKv), ("src", _p), ("src_dtype", _i32), ("norm", _i32), ("n_rows", _i64),
+                ("src_row_stride", _i64), ("weight", _p), ("rope_cs", _p), ("eps", _f32)]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = [("kv", PagedKv), ("q", _p), ("n_rows", _i64), ("q_row_stride", _i64), ("q_head_stride", _i64),
+                ("H", _i32), ("D", _i32), ("softmax_scale", _f32), ("window", _i32), ("sink", _p), ("rope_cs", _p),
+                ("out", _p), ("lse", _p)]
 
 
 class KernelTime(ctypes.Structure):
@@ -120,6 +148,10 @@ _cp_merge_ws = _sig("csa_cp_merge_workspace_size", ctypes.c_size_t, [_i32, _i32,
 _cp_merge = _sig("csa_cp_merge_topk", _i32, [_p, _p, _i32, _i32, _i32, _i32, _p, _p, ctypes.c_size_t, _p])
 _cp_localize = _sig("csa_cp_localize", _i32, [_p, _i32, _i32, _i64, _i64, _p, _p])
 _cp_combine = _sig("csa_cp_combine", _i32, [_p, _p, _i32, _i32, _i32, _p, _p, _p, _p])
+_rms_norm = _sig("csa_rms_norm", _i32, [ctypes.POINTER(RmsNormArgs), _p])
+_paged_append = _sig("csa_paged_append", _i32, [ctypes.POINTER(PagedAppendArgs), _p])
+_paged_attn_ws = _sig("csa_paged_attn_workspace_size", ctypes.c_size_t, [ctypes.POINTER(PagedAttnArgs)])
+_paged_attn = _sig("csa_paged_attn", _i32, [ctypes.POINTER(PagedAttnArgs), _p, ctypes.c_size_t, _p])
 
 EXPORTED = ["csa_quant_kv", "csa_compress_kv", "csa_quant_mxfp4", "csa_index_workspace_size", "csa_index_topk", "csa_topk_workspace_size",
             "csa_topk_scores", "csa_attn_workspace_size", "csa_sparse_attn", "csa_layer_workspace_size",
@@ -127,7 +159,8 @@ EXPORTED = ["csa_quant_kv", "csa_compress_kv", "csa_quant_mxfp4", "csa_index_wor
             "csa_profile_enable", "csa_profile_collect", "csa_index_topk_noalloc", "csa_device_status",
             "csa_index_noalloc_capacity", "csa_profile_snapshot", "csa_profile_reset",
             "csa_bench_copy", "csa_bench_fp8_gemm", "csa_cp_local_pairs", "csa_cp_merge_workspace_size",
-            "csa_cp_merge_topk", "csa_cp_localize", "csa_cp_combine", "csa_layer_step_sync"]
+            "csa_cp_merge_topk", "csa_cp_localize", "csa_cp_combine", "csa_layer_step_sync", "csa_rms_norm", "csa_paged_append",
+            "csa_paged_attn_workspace_size", "csa_paged_attn"]
 
 
 def profile_enable(on: bool) -> bool:
@@ -294,6 +327,26 @@ def csa_sparse_attn(args: AttnArgs, workspace=None, stream=None, device=None) ->
     _check(_attn(ctypes.byref(args), _ptr(workspace), nbytes, _stream(stream)), "csa_sparse_attn")
 
 
+def csa_rms_norm(args: RmsNormArgs, stream=None) -> None:
+    _check(_rms_norm(ctypes.byref(args), _stream(stream)), "csa_rms_norm")
+
+
+def csa_paged_append(args: PagedAppendArgs, stream=None) -> None:
+    _check(_paged_append(ctypes.byref(args), _stream(stream)), "csa_paged_append")
+
+
+def csa_paged_attn_workspace_size(args: PagedAttnArgs) -> int:
+    return int(_paged_attn_ws(ctypes.byref(args)))
+
+
+def csa_paged_attn(args: PagedAttnArgs, workspace=None, stream=None, device=None) -> None:
+    # the library checks a given workspace's size itself; query it only to allocate one
+    if workspace is None:
+        workspace = _workspace(csa_paged_attn_workspace_size(args), device or "cuda")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_paged_attn(ctypes.byref(args), _ptr(workspace), nbytes, _stream(stream)), "csa_paged_attn")
+
+
 def make_layer_array(layers: Sequence[LayerDesc]):
     """ctypes array of LayerDesc.  Assigning an IndexArgs / AttnArgs /
     QuantJob into a LayerDesc copies raw pointers only: the caller keeps the
@@ -448,3 +501,131 @@ def quant_job(src, fmt: int, dst, dst_row_stride: int, n_rows: Optional[int] = N
     j.dst_row_stride = dst_row_stride
     j._keep = (src, dst)
     return j
+
+
+def _dtype_of(t, what: str) -> int:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return CSA_SRC_BF16
+    if t.dtype == torch.float32:
+        return CSA_SRC_F32
+    raise TypeError(f"{what} must be float32 or bfloat16")
+
+
+def _expect(t, dtype: str, what: str, shape=None, contiguous=False) -> None:
+    """Type, shape (None = any extent) and layout of an argument tensor."""
+    if t is None:
+        return
+    if str(t.dtype) != "torch." + dtype:
+        raise TypeError(f"{what} must be {dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape))):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+
+
+def _row_stride(t) -> int:
+    """Stride of the first dimension; a single row's is arbitrary in torch."""
+    if t.shape[0] > 1:
+        return t.stride(0)
+    n = 1
+    for size, stride in zip(t.shape[1:], t.stride()[1:]):
+        n += (size - 1) * stride
+    return max(n, 1)
+
+
+def rms_norm_args(*, x, out=None, residual=None, residual_out=None, weight=None, eps: float = 1e-6,
+                  codes=None, scales=None) -> RmsNormArgs:
+    """RmsNormArgs from torch tensors: x, residual, residual_out, out [n_rows, dim]
+    in one type (fp32 or bf16), weight fp32 [dim], codes uint8 [n_rows, dim].
+    ``scales`` picks the codes' scale rule: uint8 [n_rows, dim / 32] (UE8M0),
+    fp32 [n_rows, dim / 128], or None (plain E4M3 codes)."""
+    torch = _torch()
+    n, dim = x.shape
+    a = RmsNormArgs()
+    a.n_rows, a.dim, a.dtype = n, dim, _dtype_of(x, "x")
+    name = str(x.dtype)[6:]
+    for t, what in ((x, "x"), (residual, "residual"), (residual_out, "residual_out"), (out, "out")):
+        _expect(t, name, what, (n, dim))
+    _expect(weight, "float32", "weight", (dim,))
+    _expect(codes, "uint8", "codes", (n, dim))
+    a.scale_kind = CSA_SCALE_NONE
+    if scales is not None:
+        a.scale_kind = CSA_SCALE_UE8M0X32 if scales.dtype == torch.uint8 else CSA_SCALE_F32X128
+        block = 32 if a.scale_kind == CSA_SCALE_UE8M0X32 else 128
+        _expect(scales, "uint8" if block == 32 else "float32", "scales", (n, dim // block))
+        a.scales, a.scales_stride = _ptr(scales), _row_stride(scales)
+    a.x, a.x_stride = _ptr(x), _row_stride(x)
+    if residual is not None:
+        a.residual, a.residual_stride = _ptr(residual), _row_stride(residual)
+    if residual_out is not None:
+        a.residual_out, a.residual_out_stride = _ptr(residual_out), _row_stride(residual_out)
+    if out is not None:
+        a.out, a.out_stride = _ptr(out), _row_stride(out)
+    if codes is not None:
+        a.codes, a.codes_stride = _ptr(codes), _row_stride(codes)
+    a.weight, a.eps = _ptr(weight), eps
+    a._keep = (x, residual, residual_out, weight, out, codes, scales)
+    return a
+
+
+def paged_kv(*, pages, block_table, cu_q, kv_len) -> PagedKv:
+    """PagedKv from torch tensors: pages uint8 [n_pages, page_size, 288 or 528]
+    (the entry size picks the format; page and row strides as they are),
+    block_table int32 [B, max_pages], cu_q int32 [B + 1], kv_len int32 [B]."""
+    k = PagedKv()
+    k.n_pages, k.page_size, entry = pages.shape
+    if entry not in (FP4_ENTRY_BYTES, FP8_ENTRY_BYTES):
+        raise ValueError(f"pages hold entries of {FP4_ENTRY_BYTES} or {FP8_ENTRY_BYTES} bytes, not {entry}")
+    _expect(pages, "uint8", "pages")
+    k.B, k.max_pages = block_table.shape
+    _expect(block_table, "int32", "block_table")
+    _expect(cu_q, "int32", "cu_q", (k.B + 1,), contiguous=True)
+    _expect(kv_len, "int32", "kv_len", (k.B,), contiguous=True)
+    k.fmt = CSA_FMT_FP4_E2M1_E4M3X16 if entry == FP4_ENTRY_BYTES else CSA_FMT_FP8_E4M3_UE8M0X32
+    k.pages, k.row_stride = _ptr(pages), pages.stride(1) if k.page_size > 1 else entry
+    k.page_stride = pages.stride(0) if k.n_pages > 1 else k.page_size * k.row_stride
+    k.block_table, k.table_stride = _ptr(block_table), _row_stride(block_table)
+    k.cu_q, k.kv_len = _ptr(cu_q), _ptr(kv_len)
+    k._keep = (pages, block_table, cu_q, kv_len)
+    return k
+
+
+def paged_append_args(*, src, kv: PagedKv, norm: bool = False, weight=None, eps: float = 1e-6,
+                      rope_cs=None) -> PagedAppendArgs:
+    """PagedAppendArgs from torch tensors: src fp32 / bf16 [n_rows, 512] (the
+    packed new tokens), weight fp32 [512] (with norm), rope_cs fp32
+    [n_rows, 32, 2] (cos, sin) of each row's position."""
+    a = PagedAppendArgs()
+    a.kv = kv
+    a.src_dtype = _dtype_of(src, "src")
+    _expect(src, str(src.dtype)[6:], "src", (None, 512))
+    _expect(weight, "float32", "weight", (512,))
+    _expect(rope_cs, "float32", "rope_cs", (src.shape[0], 32, 2), contiguous=True)
+    a.src, a.n_rows, a.src_row_stride = _ptr(src), src.shape[0], _row_stride(src)
+    a.norm, a.weight, a.eps, a.rope_cs = 1 if norm else 0, _ptr(weight), eps, _ptr(rope_cs)
+    a._keep = (kv, src, weight, rope_cs)
+    return a
+
+
+def paged_attn_args(*, q, kv: PagedKv, out, softmax_scale: float, lse=None, sink=None, window: int = 0,
+                    rope_cs=None) -> PagedAttnArgs:
+    """PagedAttnArgs from torch tensors: q bf16 [n_rows, H, 512] (row and head
+    strides as they are), out bf16 [n_rows, H, 512] and lse fp32 [n_rows, H]
+    contiguous, sink fp32 [H], rope_cs fp32 [n_rows, 32, 2]; window 0 = none."""
+    a = PagedAttnArgs()
+    a.kv = kv
+    _expect(q, "bfloat16", "q", (None, None, 512))
+    a.n_rows, a.H, a.D = q.shape
+    _expect(out, "bfloat16", "out", tuple(q.shape), contiguous=True)
+    _expect(lse, "float32", "lse", (a.n_rows, a.H), contiguous=True)
+    _expect(sink, "float32", "sink", (a.H,))
+    _expect(rope_cs, "float32", "rope_cs", (a.n_rows, 32, 2), contiguous=True)
+    a.q, a.q_head_stride = _ptr(q), q.stride(1) if a.H > 1 else 512
+    a.q_row_stride = q.stride(0) if a.n_rows > 1 else a.H * a.q_head_stride
+    a.out, a.lse, a.softmax_scale, a.window = _ptr(out), _ptr(lse), softmax_scale, window
+    a.sink, a.rope_cs = _ptr(sink), _ptr(rope_cs)
+    a._keep = (kv, q, out, lse, sink, rope_cs)
+    return a

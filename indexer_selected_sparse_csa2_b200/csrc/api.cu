@@ -41,6 +41,11 @@ int read_at_error(bool clear);
 int read_pk_error(bool clear);
 cudaError_t run_sparse_attn(const csa_attn_args* a, void* ws, cudaStream_t stream, const void* q2, int share);
 bool attn_tc_path(const csa_attn_args* a);
+cudaError_t launch_rms_norm(const csa_norm_args* a, cudaStream_t stream);
+cudaError_t launch_paged_append(const csa_paged_append_args* a, cudaStream_t stream);
+size_t paged_attn_ws_bytes(const csa_paged_attn_args* a);
+cudaError_t launch_paged_attn(const csa_paged_attn_args* a, void* ws, cudaStream_t stream);
+int read_pg_error(bool clear);
 
 static bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 static bool al16i(int64_t v) { return (v & 15) == 0; }
@@ -124,6 +129,83 @@ static csa_status check_attn(const csa_attn_args* a) {
     return a->win_row_stride < kFp8Bytes ? CSA_ERR_SHAPE : CSA_ERR_ALIGNMENT;
   if (!al16(a->q) || !al16(a->out) || !al16(a->rope_cs)) return CSA_ERR_ALIGNMENT;
   if (a->out_bf16 != 0 && a->out_bf16 != 1) return CSA_ERR_INVALID_ARG;
+  return CSA_OK;
+}
+
+// Row stride (elements of esz bytes) of an optional or required 2-D operand.
+static csa_status check_rows(const void* p, int64_t stride, int64_t dim, int64_t esz) {
+  if (stride < dim) return CSA_ERR_SHAPE;
+  if (stride > ((int64_t)1 << 40)) return CSA_ERR_SHAPE;
+  return al16(p) && al16i(stride * esz) ? CSA_OK : CSA_ERR_ALIGNMENT;
+}
+
+static csa_status check_norm(const csa_norm_args* a) {
+  if (!a) return CSA_ERR_INVALID_ARG;
+  if (a->dtype != CSA_SRC_F32 && a->dtype != CSA_SRC_BF16) return CSA_ERR_INVALID_ARG;
+  if (a->scale_kind != CSA_SCALE_NONE && a->scale_kind != CSA_SCALE_UE8M0X32 && a->scale_kind != CSA_SCALE_F32X128)
+    return CSA_ERR_INVALID_ARG;
+  if (a->n_rows < 0 || a->n_rows >= ((int64_t)1 << 40)) return CSA_ERR_SHAPE;
+  if (a->n_rows == 0) return CSA_OK;
+  const int block = !a->codes || a->scale_kind == CSA_SCALE_NONE ? 16 : a->scale_kind == CSA_SCALE_UE8M0X32 ? 32 : 128;
+  if (a->dim < 16 || a->dim > 16384 || a->dim % block) return CSA_ERR_SHAPE;
+  if (!a->x || (!a->out && !a->codes) || (a->residual_out && !a->residual)) return CSA_ERR_INVALID_ARG;
+  if (a->codes && a->scale_kind != CSA_SCALE_NONE && !a->scales) return CSA_ERR_INVALID_ARG;
+  if (!(a->eps >= 0.f)) return CSA_ERR_INVALID_ARG;
+  const int64_t esz = a->dtype == CSA_SRC_BF16 ? 2 : 4;
+  csa_status s = check_rows(a->x, a->x_stride, a->dim, esz);
+  if (s == CSA_OK && a->residual) s = check_rows(a->residual, a->residual_stride, a->dim, esz);
+  if (s == CSA_OK && a->residual_out) s = check_rows(a->residual_out, a->residual_out_stride, a->dim, esz);
+  if (s == CSA_OK && a->out) s = check_rows(a->out, a->out_stride, a->dim, esz);
+  if (s == CSA_OK && a->codes) s = check_rows(a->codes, a->codes_stride, a->dim, 1);
+  if (s != CSA_OK) return s;
+  if (!al16(a->weight)) return CSA_ERR_ALIGNMENT;
+  if (a->codes && a->scale_kind != CSA_SCALE_NONE) {
+    if (a->scales_stride < a->dim / block || a->scales_stride > ((int64_t)1 << 40)) return CSA_ERR_SHAPE;
+    if (a->scale_kind == CSA_SCALE_F32X128 && ((uintptr_t)a->scales & 3)) return CSA_ERR_ALIGNMENT;
+  }
+  return CSA_OK;
+}
+
+static csa_status check_paged(const csa_paged_kv* k) {
+  if (k->fmt != CSA_FMT_FP4_E2M1_E4M3X16 && k->fmt != CSA_FMT_FP8_E4M3_UE8M0X32) return CSA_ERR_INVALID_ARG;
+  if (k->B < 1 || k->B > 65536 || k->page_size < 1 || k->page_size > 65536 || k->max_pages < 1) return CSA_ERR_SHAPE;
+  if ((int64_t)k->max_pages * k->page_size >= ((int64_t)1 << 31)) return CSA_ERR_SHAPE;
+  if (k->n_pages < 1 || k->n_pages >= ((int64_t)1 << 31) || k->table_stride < k->max_pages) return CSA_ERR_SHAPE;
+  if (!k->pages || !k->block_table || !k->cu_q || !k->kv_len) return CSA_ERR_INVALID_ARG;
+  const int64_t bytes = k->fmt == CSA_FMT_FP4_E2M1_E4M3X16 ? kFp4Bytes : kFp8Bytes;
+  if (k->row_stride < bytes || k->row_stride > ((int64_t)1 << 40) || k->page_stride < 0) return CSA_ERR_SHAPE;
+  if (!al16(k->pages) || !al16i(k->row_stride) || !al16i(k->page_stride)) return CSA_ERR_ALIGNMENT;
+  if (((uintptr_t)k->block_table & 3) || ((uintptr_t)k->cu_q & 3) || ((uintptr_t)k->kv_len & 3)) return CSA_ERR_ALIGNMENT;
+  return CSA_OK;
+}
+
+static csa_status check_paged_append(const csa_paged_append_args* a) {
+  if (!a) return CSA_ERR_INVALID_ARG;
+  const csa_status s = check_paged(&a->kv);
+  if (s != CSA_OK) return s;
+  if (a->src_dtype != CSA_SRC_F32 && a->src_dtype != CSA_SRC_BF16) return CSA_ERR_INVALID_ARG;
+  if (a->norm != 0 && a->norm != 1) return CSA_ERR_INVALID_ARG;
+  if (a->n_rows < 0 || a->n_rows >= ((int64_t)1 << 31)) return CSA_ERR_SHAPE;
+  if (a->n_rows == 0) return CSA_OK;
+  if (!a->src || (a->weight && !a->norm)) return CSA_ERR_INVALID_ARG;
+  if (a->norm && !(a->eps >= 0.f)) return CSA_ERR_INVALID_ARG;
+  if (!al16(a->weight) || !al16(a->rope_cs)) return CSA_ERR_ALIGNMENT;
+  return check_rows(a->src, a->src_row_stride, kD, a->src_dtype == CSA_SRC_BF16 ? 2 : 4);
+}
+
+static csa_status check_paged_attn(const csa_paged_attn_args* a) {
+  if (!a) return CSA_ERR_INVALID_ARG;
+  const csa_status s = check_paged(&a->kv);
+  if (s != CSA_OK) return s;
+  if (a->H < 1 || a->H > 128 || a->D != kD || a->window < 0) return CSA_ERR_SHAPE;
+  if (a->n_rows < 0 || a->n_rows * (int64_t)a->H >= ((int64_t)1 << 31) || a->n_rows >= ((int64_t)1 << 31)) return CSA_ERR_SHAPE;
+  if (a->n_rows == 0) return CSA_OK;
+  if (!a->q || !a->out) return CSA_ERR_INVALID_ARG;
+  if (!(a->softmax_scale >= 0.f) || !(a->softmax_scale <= 3.0e38f)) return CSA_ERR_INVALID_ARG;
+  if (a->q_head_stride < kD || a->q_row_stride < 0) return CSA_ERR_SHAPE;
+  if (!al16(a->q) || !al16i(a->q_row_stride * 2) || !al16i(a->q_head_stride * 2) || !al16(a->out) || !al16(a->rope_cs))
+    return CSA_ERR_ALIGNMENT;
+  if (((uintptr_t)a->sink & 3) || ((uintptr_t)a->lse & 3)) return CSA_ERR_ALIGNMENT;
   return CSA_OK;
 }
 
@@ -237,6 +319,32 @@ csa_status csa_sparse_attn(const csa_attn_args* a, void* workspace, size_t works
   if (need > workspace_bytes || (need && !workspace)) return CSA_ERR_WORKSPACE;
   if (need && !al16(workspace)) return CSA_ERR_ALIGNMENT;
   return from_cuda(run_sparse_attn(a, workspace, (cudaStream_t)stream, nullptr, 1));
+}
+
+csa_status csa_rms_norm(const csa_norm_args* a, csa_stream_t stream) {
+  const csa_status s = check_norm(a);
+  if (s != CSA_OK || a->n_rows == 0) return s;
+  return from_cuda(launch_rms_norm(a, (cudaStream_t)stream));
+}
+
+csa_status csa_paged_append(const csa_paged_append_args* a, csa_stream_t stream) {
+  const csa_status s = check_paged_append(a);
+  if (s != CSA_OK || a->n_rows == 0) return s;
+  return from_cuda(launch_paged_append(a, (cudaStream_t)stream));
+}
+
+size_t csa_paged_attn_workspace_size(const csa_paged_attn_args* a) {
+  if (check_paged_attn(a) != CSA_OK || a->n_rows == 0) return 0;
+  return paged_attn_ws_bytes(a);
+}
+
+csa_status csa_paged_attn(const csa_paged_attn_args* a, void* workspace, size_t workspace_bytes,
+                          csa_stream_t stream) {
+  const csa_status s = check_paged_attn(a);
+  if (s != CSA_OK || a->n_rows == 0) return s;
+  if (!workspace || workspace_bytes < paged_attn_ws_bytes(a)) return CSA_ERR_WORKSPACE;
+  if (!al16(workspace)) return CSA_ERR_ALIGNMENT;
+  return from_cuda(launch_paged_attn(a, workspace, (cudaStream_t)stream));
 }
 
 // Layers that run the indexer (Full, Reindex); Reuse and SWA layers do not.
@@ -624,8 +732,8 @@ const char* csa_status_string(int32_t s) {
 
 int32_t csa_device_status(void) {
   const int a = read_tc_error(true), b = read_pf_error(true), c = read_at_error(true);
-  const int d = read_pk_error(true), e = read_mx_error(true);
-  return (int32_t)(a ? a : (b ? b : (c ? c : (d ? d : e))));
+  const int d = read_pk_error(true), e = read_mx_error(true), f = read_pg_error(true);
+  return (int32_t)(a ? a : (b ? b : (c ? c : (d ? d : (e ? e : f)))));
 }
 
 uint64_t csa_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

@@ -1,0 +1,997 @@
+// MLA attention of packed chunks of new tokens over a paged latent cache
+// (csa_paged_attn_args in csa.h): causal, optional sliding window, sink and
+// partial RoPE, FP8 or FP4 entries, one token per sequence up to whole prompts.
+//
+// A work item is 64 query rows (token, head) of one sequence, rows in (token,
+// head) order, so any head count fills the tile; it runs over the 64-entry
+// key tiles its rows see.  Per key tile, with K = V = the decoded entries:
+//   S  = Q K^T    tcgen05.mma kind::f16, M = 128 TMEM lanes holding the 64
+//                 rows twice (lane L: row L mod 64), N = 64 entries, K = 512.
+//                 Channels 0..383 of Q are the A operand in TMEM, the last
+//                 128 in shared memory.  The two copies let four softmax
+//                 warps share a tile: warps 0-1 take entries 0..31 of rows
+//                 0..63, warps 2-3 entries 32..63.
+//   O^T += V^T P^T  M = 128 latent channels (4 chunks), N = 64 rows, K = 64
+//                 entries: 4 x 64 TMEM columns, where O (64 x 512) would take
+//                 all 512.  The shared-memory tile of decoded entries is the
+//                 K-major B operand of S and the MN-major A operand here.
+// Online softmax in the exp2 domain; the running max moves only when a tile's
+// max exceeds it by more than 8, and only then O^T is rescaled in TMEM.  P is
+// held in fp16 times 2^6: at most 2^14, and weights down to 2^-31 of the max
+// keep a value.
+//
+// Work split: every key tile of every item is one unit (an item that sees no
+// entry is one unit too); CTA i takes units [iU/G, (i+1)U/G) of the batch in
+// order, whatever the sequences' lengths, and computes where that is from the
+// lengths on the device.  An item that ends up in several CTAs leaves
+// (max, sum, O^T) partials in the workspace, at most two per CTA, which
+// paged_attn_combine joins in CTA order; the result does not depend on timing.
+//
+// Warp roles: 0-3 softmax and output, 4-11 entry loads and decoding, and the
+// staging of Q at the start of an item, 12 issues the S MMAs, 13 the PV MMAs.
+// Entry tiles and P are double buffered; the entries of tile t + 1 are loaded
+// into registers as tile t's are decoded, page table values one tile earlier.
+#include <climits>
+
+#include "sm100.cuh"
+#include "paged.cuh"
+#include "rope.cuh"
+
+namespace csa {
+
+constexpr int kPgRows = 64;               // query rows per item
+constexpr int kPgE = 64;                  // entries per key tile
+constexpr int kPgDeqWarps = 8;
+constexpr int kPgWarpS = 4 + kPgDeqWarps;
+constexpr int kPgWarpPV = kPgWarpS + 1;
+constexpr int kPgWarps = kPgWarpPV + 1;
+constexpr int kPgThreads = 32 * kPgWarps;
+constexpr int kPgQTmemBlocks = 6;         // 64-channel blocks of Q in TMEM
+constexpr int kPgQBlk = 128 * 128;        // shared Q block: 128 rows x 64 fp16
+constexpr int kPgKVBlk = kPgE * 128;      // 64-channel block of an entry tile
+constexpr int kPgKVBytes = 8 * kPgKVBlk;
+constexpr int kPgPBytes = kPgRows * kPgE * 2;
+constexpr uint32_t kPgSCol = 32 * kPgQTmemBlocks;
+constexpr uint32_t kPgOCol = 256;
+constexpr uint32_t kPgTmemCols = 512;
+constexpr float kPgRescale = 8.0f;        // lazy-rescale threshold (exp2 units)
+constexpr float kPgPExp = 6.0f;           // P carries a factor 2^6
+constexpr float kPgLog2e = 1.4426950408889634f;
+constexpr float kPgLn2 = 0.6931471805599453f;
+constexpr int kPgMaxB = 65536;
+constexpr size_t kPgSmemBytes = 1024 + 2 * kPgQBlk + 2 * kPgKVBytes + 2 * kPgPBytes + 4096;
+static_assert(kPgMaxB / 32 * 8 <= 2 * kPgKVBytes, "the plan's group sums use the entry tiles");
+
+static __device__ int g_pg_error;
+
+// What a CTA left for the combine.
+struct PgMeta {
+  int64_t row0;      // leader: first output row (token * H + head) of its last item
+  int32_t rows;      // leader: rows of that item; 0 = its last item is not split here
+  int32_t cont;      // its first item began in an earlier CTA ...
+  int32_t done;      // ... and ends here
+  int32_t pad;
+};
+
+struct PgParams {
+  csa_paged_attn_args a;
+  float scale_log2;  // softmax_scale * log2(e), times the entries' staging factor
+  float out_scale;   // inverse of the entries' staging factor
+  float* part_o;     // [2 * gridDim.x][64][512] fp32
+  float2* part_ml;   // [2 * gridDim.x][64] (max, sum)
+  PgMeta* meta;      // [gridDim.x]
+};
+
+struct PgSmem {
+  uint8_t* q;        // channels 384..511 of Q: 2 blocks of 128 rows
+  uint8_t* kv;       // 2 entry tiles
+  uint8_t* p;        // 2 x P
+  float* mx;         // [2][2][64] tile maxima by tile parity and entry half
+  float* alpha;      // [64] rescale factors
+  float* lx;         // [2][64] sums of the entry halves
+  float* scl;        // [64] output factors
+  uint32_t* valid;   // [2][2] entries present, by tile parity
+  int64_t* start;    // this CTA's range: {first unit's offset in its item, units, sequence, tile}
+  uint64_t* bars;
+  uint32_t* tmem_base;
+};
+
+CSA_DEV PgSmem carve_pg(uint8_t* raw) {
+  PgSmem s;
+  uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  s.q = p; p += 2 * kPgQBlk;
+  s.kv = p; p += 2 * kPgKVBytes;
+  s.p = p; p += 2 * kPgPBytes;
+  s.mx = reinterpret_cast<float*>(p); p += 4 * 64 * 4;
+  s.alpha = reinterpret_cast<float*>(p); p += 64 * 4;
+  s.lx = reinterpret_cast<float*>(p); p += 2 * 64 * 4;
+  s.scl = reinterpret_cast<float*>(p); p += 64 * 4;
+  s.bars = reinterpret_cast<uint64_t*>(p); p += 16 * 8;
+  s.start = reinterpret_cast<int64_t*>(p); p += 4 * 8;
+  s.valid = reinterpret_cast<uint32_t*>(p); p += 4 * 4;
+  s.tmem_base = reinterpret_cast<uint32_t*>(p);
+  return s;
+}
+
+CSA_DEV uint32_t pg_h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+CSA_DEV __half2 pg_u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+CSA_DEV float pg_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Bounded wait by a whole warp, the same answer in every lane.
+CSA_DEV bool pg_wait_warp(uint64_t* bar, uint32_t parity, int code) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_pg_error, code));
+}
+
+// ------------------------------------------------------------- work items --
+struct PgSeq {
+  int n;        // new tokens
+  int kv;       // cache length with them, >= 0
+  int row0;     // first packed row
+  int tiles;    // items of 64 (token, head) rows
+};
+CSA_DEV PgSeq pg_seq(const csa_paged_attn_args& a, int b) {
+  PgSeq s;
+  const int hi = (int)a.n_rows;
+  s.row0 = min(max(a.kv.cu_q[b], 0), hi);
+  s.n = min(max(a.kv.cu_q[b + 1], s.row0), hi) - s.row0;
+  s.kv = max(a.kv.kv_len[b], 0);
+  s.tiles = (int)(((int64_t)s.n * a.H + kPgRows - 1) / kPgRows);
+  return s;
+}
+// Positions [k0, k1) that the rows of item j see (k1 = k0: none), before the
+// rows' own masks.  Row r of the item is (token, head) row 64 j + r.
+CSA_DEV void pg_item(const csa_paged_attn_args& a, const PgSeq& s, int j, int& k0, int& k1) {
+  const int r0 = j * kPgRows, r1 = min(r0 + kPgRows, s.n * a.H) - 1;
+  const int p0 = s.kv - s.n + r0 / a.H, p1 = s.kv - s.n + r1 / a.H;
+  k1 = min(p1 + 1, a.kv.max_pages * a.kv.page_size);
+  k0 = a.window ? max(0, p0 + 1 > a.window ? p0 + 1 - a.window : 0) : 0;
+  if (k1 < k0) k1 = k0;
+}
+CSA_DEV int pg_units(int k0, int k1) { return max(1, (k1 - k0 + kPgE - 1) / kPgE); }
+
+// The CTA's walk over its items.
+struct PgWalk {
+  int64_t left;    // units left, this item's included
+  int b, j, off;   // sequence, item, first key tile of the item taken here
+  PgSeq s;
+  int k0, k1, units, take;   // take: units of this item taken here
+  CSA_DEV void item(const csa_paged_attn_args& a) {
+    pg_item(a, s, j, k0, k1);
+    units = pg_units(k0, k1);
+    take = (int)min((int64_t)(units - off), left);
+  }
+  CSA_DEV bool begin(const csa_paged_attn_args& a, const int64_t* start) {
+    off = (int)start[0];
+    left = start[1];
+    b = (int)start[2];
+    j = (int)start[3];
+    if (left <= 0) return false;
+    s = pg_seq(a, b);
+    item(a);
+    return true;
+  }
+  CSA_DEV int tiles() const { return k1 > k0 ? take : 0; }
+  CSA_DEV bool next(const csa_paged_attn_args& a) {
+    left -= take;
+    if (left <= 0) return false;
+    off = 0;
+    if (++j >= s.tiles) {
+      j = 0;
+      do {
+        if (++b >= a.kv.B) { left = 0; return false; }
+        s = pg_seq(a, b);
+      } while (s.tiles == 0);
+    }
+    item(a);
+    return true;
+  }
+};
+
+CSA_DEV int64_t pg_warp_sum64(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// Units of sequences 32 g + lane (0 past the last).  Sequences with many
+// items are summed by the whole warp.
+CSA_DEV int64_t pg_group_units(const csa_paged_attn_args& a, int g, int lane) {
+  const int b = 32 * g + lane;
+  PgSeq s{0, 0, 0, 0};
+  if (b < a.kv.B) s = pg_seq(a, b);
+  int64_t u = 0;
+  if (s.tiles <= 4) {
+    for (int j = 0; j < s.tiles; ++j) {
+      int k0, k1;
+      pg_item(a, s, j, k0, k1);
+      u += pg_units(k0, k1);
+    }
+  }
+  for (uint32_t big = __ballot_sync(0xffffffffu, s.tiles > 4); big; big &= big - 1) {
+    const int l = __ffs(big) - 1;
+    PgSeq q;
+    q.n = __shfl_sync(0xffffffffu, s.n, l);
+    q.kv = __shfl_sync(0xffffffffu, s.kv, l);
+    q.row0 = 0;
+    q.tiles = __shfl_sync(0xffffffffu, s.tiles, l);
+    int64_t v = 0;
+    for (int j = lane; j < q.tiles; j += 32) {
+      int k0, k1;
+      pg_item(a, q, j, k0, k1);
+      v += pg_units(k0, k1);
+    }
+    v = pg_warp_sum64(v);
+    if (lane == l) u = v;
+  }
+  return u;
+}
+// Lane whose value the running sum `at` (0 <= at < the warp's sum) falls in;
+// `at` becomes the offset inside it.  v >= 0.
+CSA_DEV int pg_locate(int64_t v, int64_t& at, int lane) {
+  int64_t inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  const int l = __ffs(__ballot_sync(0xffffffffu, at < inc)) - 1;
+  const int64_t before = __shfl_sync(0xffffffffu, inc - v, l < 0 ? 0 : l);
+  at -= before;
+  return l < 0 ? 0 : l;
+}
+// Finds the CTA's range of units; every warp of the CTA takes part.
+CSA_DEV void pg_plan(const csa_paged_attn_args& a, const PgSmem& S, int warp, int lane) {
+  int64_t* gsum = reinterpret_cast<int64_t*>(S.kv);
+  const int groups = (a.kv.B + 31) / 32;
+  for (int g = warp; g < groups; g += kPgWarps) {
+    const int64_t u = pg_warp_sum64(pg_group_units(a, g, lane));
+    if (lane == 0) gsum[g] = u;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int64_t total = 0;
+    for (int g = lane; g < groups; g += 32) total += gsum[g];
+    total = pg_warp_sum64(total);
+    const int64_t G = min((int64_t)gridDim.x, total);
+    int64_t u0 = 0, u1 = 0;
+    if ((int64_t)blockIdx.x < G) {
+      u0 = total * blockIdx.x / G;
+      u1 = total * (blockIdx.x + 1) / G;
+    }
+    int64_t at = u0;
+    int b = 0, j = 0;
+    if (u1 > u0) {
+      int base = 0;
+      for (;; base += 32) {                                // the 32 groups
+        const int64_t v = base + lane < groups ? gsum[base + lane] : 0;
+        const int64_t sum = pg_warp_sum64(v);
+        if (at < sum || base + 32 >= groups) {
+          base += pg_locate(v, at, lane);
+          break;
+        }
+        at -= sum;
+      }
+      const int64_t v = pg_group_units(a, base, lane);     // the sequence
+      b = 32 * base + pg_locate(v, at, lane);
+      const PgSeq s = pg_seq(a, b);
+      for (;; j += 32) {                                   // the item
+        int64_t w = 0;
+        if (j + lane < s.tiles) {
+          int k0, k1;
+          pg_item(a, s, j + lane, k0, k1);
+          w = pg_units(k0, k1);
+        }
+        const int64_t sum = pg_warp_sum64(w);
+        if (at < sum || j + 32 >= s.tiles) {
+          j += pg_locate(w, at, lane);
+          break;
+        }
+        at -= sum;
+      }
+    }
+    if (lane == 0) {
+      S.start[0] = at;
+      S.start[1] = u1 - u0;
+      S.start[2] = b;
+      S.start[3] = j;
+    }
+  }
+  __syncthreads();
+}
+
+// --------------------------------------------------------------- decoding --
+// Operand channel order.  Inside every group of 8 channels the staged K, V
+// and Q hold them in the order in which shifts and masks produce fp16 pairs
+// from a word of codes: FP8 words of 4 codes give (0, 2), (1, 3); FP4 words
+// of 8 codes give (0, 4), (1, 5), (2, 6), (3, 7).  S does not depend on the
+// order, and the output undoes it.
+template <bool FP4>
+CSA_DEV int pg_channel(int pos) {   // channel at operand position pos
+  return FP4 ? (pos & ~7) | ((pos & 7) >> 1) | ((pos & 1) << 2)
+             : (pos & ~3) | ((pos & 3) >> 1) | ((pos & 1) << 1);
+}
+// 8 query channels as four operand words.
+template <bool FP4>
+CSA_DEV void pg_q_words(const float (&f)[8], uint32_t (&o)[4]) {
+  if (FP4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = pg_h2u(__floats2half2_rn(f[k], f[k + 4]));
+  } else {
+    o[0] = pg_h2u(__floats2half2_rn(f[0], f[2]));
+    o[1] = pg_h2u(__floats2half2_rn(f[1], f[3]));
+    o[2] = pg_h2u(__floats2half2_rn(f[4], f[6]));
+    o[3] = pg_h2u(__floats2half2_rn(f[5], f[7]));
+  }
+}
+CSA_DEV void pg_bf16x8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = __uint_as_float(w[k] << 16);
+    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+}
+// E4M3 codes in bytes 0 and 2 (and 1 and 3) of w as fp16 pairs E4M3 * 2^-8:
+// exponent and mantissa move to bits 7..13, the sign to bit 15; subnormals
+// land on subnormals, so every code is exact.
+CSA_DEV uint32_t pg_e4m3_02(uint32_t w) { return ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u); }
+CSA_DEV uint32_t pg_e4m3_13(uint32_t w) { return ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u); }
+// 16 codes of one FP8 block half -> two 8-channel chunks of fp16 values.
+CSA_DEV void pg_decode_fp8(const uint4& v, int ex, uint4& c0, uint4& c1) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t o[8];
+  if (ex >= 105 && ex <= 134) {
+    // (E4M3 * 2^-8) * 2^(ex - 119), a power of two that fp16 holds
+    const uint32_t f = (uint32_t)(ex - 104) << 10;
+    const __half2 f2 = pg_u2h(f | (f << 16));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      o[2 * k] = pg_h2u(__hmul2(pg_u2h(pg_e4m3_02(w[k])), f2));
+      o[2 * k + 1] = pg_h2u(__hmul2(pg_u2h(pg_e4m3_13(w[k])), f2));
+    }
+  } else {
+    // scales far from 1: fp32 product, rounded to fp16
+    const float f = exp2f((float)(ex - 119));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = __half22float2(pg_u2h(pg_e4m3_02(w[k]))), b = __half22float2(pg_u2h(pg_e4m3_13(w[k])));
+      o[2 * k] = pg_h2u(__floats2half2_rn(a.x * f, a.y * f));
+      o[2 * k + 1] = pg_h2u(__floats2half2_rn(b.x * f, b.y * f));
+    }
+  }
+  c0 = make_uint4(o[0], o[1], o[2], o[3]);
+  c1 = make_uint4(o[4], o[5], o[6], o[7]);
+}
+// One word of 8 FP4 codes with block scale s2 = (E4M3 scale) * 2^7 -> 8 fp16
+// values E2M1 * s * 2^-7 (at most 6 significant bits and >= 2^-17: exact).
+template <int kk>
+CSA_DEV uint32_t pg_e2m1_pair(uint32_t w) {   // codes kk and kk + 4 as E2M1 * 2^-14
+  const uint32_t mag = kk < 3 ? (w << (9 - 4 * kk)) : (w >> 3);
+  const uint32_t sgn = w << (12 - 4 * kk);
+  return (mag & 0x0E000E00u) | (sgn & 0x80008000u);
+}
+CSA_DEV uint4 pg_decode_fp4(uint32_t w, __half2 s2) {
+  return make_uint4(pg_h2u(__hmul2(pg_u2h(pg_e2m1_pair<0>(w)), s2)), pg_h2u(__hmul2(pg_u2h(pg_e2m1_pair<1>(w)), s2)),
+                    pg_h2u(__hmul2(pg_u2h(pg_e2m1_pair<2>(w)), s2)), pg_h2u(__hmul2(pg_u2h(pg_e2m1_pair<3>(w)), s2)));
+}
+CSA_DEV __half2 pg_fp4_scale(uint32_t code) {   // E4M3 scale * 2^7, twice
+  return __hmul2(pg_u2h(pg_e4m3_02(code | (code << 16))), pg_u2h(0x78007800u));
+}
+
+// A position in the CTA's list of key tiles.
+struct PgCursor {
+  PgWalk w;
+  int i;           // tile of the item
+  bool live;
+  CSA_DEV void settle(const csa_paged_attn_args& a) {   // skip items that see no entry
+    while (live && w.tiles() == 0) live = w.next(a);
+  }
+  CSA_DEV void begin(const csa_paged_attn_args& a, const int64_t* start) {
+    live = w.begin(a, start);
+    i = 0;
+    settle(a);
+  }
+  CSA_DEV void advance(const csa_paged_attn_args& a) {
+    if (!live) return;
+    if (++i < w.tiles()) return;
+    i = 0;
+    live = w.next(a);
+    settle(a);
+  }
+};
+
+template <bool FP4>
+__global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_constant__ PgParams p) {
+  constexpr int kScaleOff = FP4 ? 256 : 512;
+  pdl_trigger();
+  extern __shared__ uint8_t smem_raw[];
+  const PgSmem S = carve_pg(smem_raw);
+  uint64_t* kv_full = S.bars + 0;    // [2] tile decoded (8 warp arrivals)
+  uint64_t* kv_free = S.bars + 2;    // [2] PV done: entry tile and P reusable
+  uint64_t* s_full = S.bars + 4;     // S in TMEM
+  uint64_t* s_free = S.bars + 5;     // S read by the softmax (4 warp arrivals)
+  uint64_t* p_full = S.bars + 6;     // [2] P written, O^T rescaled (4 warp arrivals)
+  uint64_t* o_done = S.bars + 8;     // one phase per PV
+  uint64_t* q_full = S.bars + 9;     // an item's Q staged (8 warp arrivals)
+  uint64_t* q_free = S.bars + 10;    // an item's last S done
+  uint64_t* acc_done = S.bars + 11;  // an item's last PV done (one phase per item)
+  uint64_t* drain = S.bars + 12;     // [2] all MMAs of an issuer retired (teardown)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const csa_paged_attn_args& a = p.a;
+  if (tid == 0) {
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(kv_full + k, kPgDeqWarps);
+      mbar_init(kv_free + k, 1);
+      mbar_init(p_full + k, 4);
+      mbar_init(drain + k, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(o_done, 1);
+    mbar_init(q_full, kPgDeqWarps);
+    mbar_init(q_free, 1);
+    mbar_init(acc_done, 1);
+    fence_mbar_init();
+  }
+  if (warp == kPgWarpS) tmem_alloc(S.tmem_base, kPgTmemCols);
+  pdl_wait();
+  pg_plan(a, S, warp, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *S.tmem_base;
+
+  if (warp == kPgWarpS) {
+    // ------------------------------------------------------------ S issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_make(kFmtF16, kFmtF16, 128, kPgE);
+      const uint32_t qa = smem_u32(S.q), kva = smem_u32(S.kv);
+      PgWalk w;
+      uint32_t t = 0, seg = 0;
+      bool ok = true;
+      for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
+        const int nt = w.tiles();
+        if (nt == 0) continue;
+        ok = mbar_wait(q_full, seg & 1u, &g_pg_error, kErrWaitTmaFull);
+        for (int i = 0; i < nt && ok; ++i, ++t) {
+          const uint32_t bi = t & 1u;
+          ok = mbar_wait(kv_full + bi, (t >> 1) & 1u, &g_pg_error, kErrWaitTmaFull);
+          if (ok && t >= 1) ok = mbar_wait(s_free, (t - 1) & 1u, &g_pg_error, kErrWaitAccEmpty);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t kvt = kva + bi * kPgKVBytes;
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            const uint32_t kb = ks >> 2, sub = ks & 3;
+            const uint64_t bd = desc_k_sw128(kvt + kb * kPgKVBlk + sub * 32);
+            if (kb < (uint32_t)kPgQTmemBlocks)
+              mma_f16_ts(tbase + kPgSCol, tbase + kb * 32 + sub * 8, bd, idesc, ks > 0 ? 1u : 0u);
+            else
+              mma_f16_ss(tbase + kPgSCol, desc_k_sw128(qa + (kb - kPgQTmemBlocks) * kPgQBlk + sub * 32), bd, idesc, 1u);
+          }
+          mma_commit(s_full);
+        }
+        if (ok) mma_commit(q_free);
+        ++seg;
+      }
+      mma_commit(drain);
+      mbar_wait(drain, 0u, &g_pg_error, kErrWaitAccFull);
+    }
+  } else if (warp == kPgWarpPV) {
+    // ----------------------------------------------------------- PV issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_make_amn(kFmtF16, kFmtF16, 128, kPgRows);
+      const uint32_t kva = smem_u32(S.kv), pa = smem_u32(S.p);
+      PgWalk w;
+      uint32_t t = 0;
+      bool ok = true;
+      for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
+        const int nt = w.tiles();
+        for (int i = 0; i < nt; ++i, ++t) {
+          const uint32_t bi = t & 1u;
+          ok = mbar_wait(p_full + bi, (t >> 1) & 1u, &g_pg_error, kErrWaitAccFull);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t kvt = kva + bi * kPgKVBytes, pb = pa + bi * kPgPBytes;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int ks = 0; ks < kPgE / 16; ++ks)
+              mma_f16_ss(tbase + kPgOCol + 64u * c,
+                         desc_mn_sw128(kvt + (uint32_t)(2 * c) * kPgKVBlk + (uint32_t)ks * 2048, kPgKVBlk, 1024),
+                         desc_k_sw128(pb + (uint32_t)ks * 32), idesc, (i > 0 || ks > 0) ? 1u : 0u);
+          }
+          mma_commit(kv_free + bi);
+          mma_commit(o_done);
+        }
+        if (nt > 0 && ok) mma_commit(acc_done);
+      }
+      mma_commit(drain + 1);
+      mbar_wait(drain + 1, 0u, &g_pg_error, kErrWaitAccFull);
+    }
+  } else if (warp >= 4) {
+    // ---------------------------------------- entry loads, decoding, Q staging
+    const int wq = warp - 4;
+    PgCursor cu;                       // the tile whose page table values are fetched next
+    cu.begin(a, S.start);
+    // page id (-1: no entry) and entry number in the page, of entry
+    // 8 wq + (lane & 7) of the tile whose entries are loaded next
+    int id = -1;
+    uint32_t slot = 0;
+    auto lookup = [&]() {
+      id = -1;
+      if (cu.live) {
+        const int pos = cu.w.k0 + (cu.w.off + cu.i) * kPgE + 8 * wq + (lane & 7);
+        if (pos < cu.w.k1) {
+          const uint32_t pg = (uint32_t)pos / (uint32_t)a.kv.page_size;
+          slot = (uint32_t)pos - pg * (uint32_t)a.kv.page_size;
+          id = a.kv.block_table[(int64_t)cu.w.b * a.kv.table_stride + pg];
+        }
+      }
+    };
+    auto entry_ptr = [&]() -> const uint8_t* {
+      return id >= 0 && id < a.kv.n_pages ? a.kv.pages + (int64_t)id * a.kv.page_stride + (int64_t)slot * a.kv.row_stride
+                                          : nullptr;
+    };
+    constexpr int kN = FP4 ? 4 : 8;    // 16-byte words per lane and tile
+    uint4 r[kN];
+    uint2 sc = make_uint2(0, 0), scn = make_uint2(0, 0);
+    uint32_t vb = 0, vbn = 0;          // valid entries of this warp's 8
+    // FP8: word k is bytes [16 lane, 16 lane + 16) of entry k; FP4: bytes
+    // [16 (lane & 15), ..) of entry 2k + (lane >> 4)
+    auto load_word = [&](const uint8_t* ptr, int k) -> uint4 {
+      const int e = FP4 ? 2 * k + (lane >> 4) : k;
+      const uint8_t* q = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)ptr, e));
+      return q ? ld_nc_v4(q + 16 * (FP4 ? lane & 15 : lane)) : make_uint4(0, 0, 0, 0);
+    };
+    // scales: lane 4e + w holds word w of entry e's scale bytes
+    auto load_scales = [&](const uint8_t* ptr) -> uint2 {
+      const uint8_t* q = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)ptr, lane >> 2));
+      if (!q) return make_uint2(0, 0);
+      if (FP4) return *reinterpret_cast<const uint2*>(q + kScaleOff + 8 * (lane & 3));
+      return make_uint2(*reinterpret_cast<const uint32_t*>(q + kScaleOff + 4 * (lane & 3)), 0);
+    };
+    // the tile being decoded
+    PgCursor dc = cu;
+    lookup();
+    {
+      const uint8_t* ptr = entry_ptr();
+      vb = __ballot_sync(0xffffffffu, ptr != nullptr) & 0xFFu;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) r[k] = load_word(ptr, k);
+      sc = load_scales(ptr);
+    }
+    cu.advance(a);
+    lookup();
+    uint32_t t = 0, seg = 0;
+    for (; dc.live; ++t) {
+      if (dc.i == 0) {
+        // ------------------------------------------------- an item begins: Q
+        if (seg > 0 && !pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty)) break;
+        tc_fence_after();
+        const PgWalk& w = dc.w;
+        const int n_rows = w.s.n * a.H - w.j * kPgRows;    // rows left in the sequence from this item on
+        const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q);
+        auto q_row = [&](int rr) -> const __nv_bfloat16* {
+          const int ri = w.j * kPgRows + rr, tok = ri / a.H;
+          return qb + (int64_t)(w.s.row0 + tok) * a.q_row_stride + (int64_t)(ri - tok * a.H) * a.q_head_stride;
+        };
+        {
+          const int rr = (32 * (warp & 3) + lane) & 63;
+          const bool on = rr < n_rows;
+          const uint4* src = reinterpret_cast<const uint4*>(q_row(on ? rr : 0)) + 24 * (wq >> 2);
+#pragma unroll 1
+          for (int u = 0; u < 6; u += 2) {                 // 32 columns: 64 channels
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = on ? src[4 * u + k] : make_uint4(0, 0, 0, 0);
+            uint32_t o[2][16];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float f[8];
+              uint32_t ow[4];
+              pg_bf16x8(v[k], f);
+              pg_q_words<FP4>(f, ow);
+#pragma unroll
+              for (int m = 0; m < 4; ++m) o[k >> 2][4 * (k & 3) + m] = ow[m];
+            }
+            const uint32_t ta = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + 96u * (wq >> 2) + 16u * u;
+            tmem_st16(ta, o[0]);
+            tmem_st16(ta + 16, o[1]);
+          }
+          tmem_wait_st();
+        }
+        {
+          const int st = 32 * wq + lane;                   // 256 threads
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = (st >> 4) + 16 * k;
+            v[k] = rr < n_rows ? *reinterpret_cast<const uint4*>(q_row(rr) + 384 + 8 * (st & 15)) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = (st >> 4) + 16 * k, c16 = st & 15;
+            float f[8];
+            pg_bf16x8(v[k], f);
+            if (a.rope_cs && c16 >= 8 && rr < n_rows) {    // channels 448 + 8 (c16 - 8) ..
+              const int tok = w.s.row0 + (w.j * kPgRows + rr) / a.H;
+              const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * (c16 - 8));
+              const float4 ca = cs[0], cb = cs[1];
+              float2 g;
+              g = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = g.x; f[1] = g.y;
+              g = rope_fwd(f[2], f[3], ca.z, ca.w); f[2] = g.x; f[3] = g.y;
+              g = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = g.x; f[5] = g.y;
+              g = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = g.x; f[7] = g.y;
+            }
+            uint32_t ow[4];
+            pg_q_words<FP4>(f, ow);
+            const uint4 o = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+            uint8_t* blk = S.q + (c16 >> 3) * kPgQBlk;
+            *reinterpret_cast<uint4*>(blk + sw128_offset_h(rr, 8 * (c16 & 7))) = o;
+            *reinterpret_cast<uint4*>(blk + sw128_offset_h(rr + 64, 8 * (c16 & 7))) = o;
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        ++seg;
+      }
+      // ------------------------------------------------------- decode the tile
+      const uint32_t bi = t & 1u;
+      const uint8_t* nptr = entry_ptr();                   // entries of the next tile (nullptr: none)
+      vbn = __ballot_sync(0xffffffffu, nptr != nullptr) & 0xFFu;
+      cu.advance(a);
+      lookup();                                            // table values of the one after
+      scn = load_scales(nptr);
+      if (t >= 2 && !pg_wait_warp(kv_free + bi, ((t >> 1) - 1) & 1u, kErrWaitSmemEmpty)) break;
+      uint8_t* kt = S.kv + bi * kPgKVBytes;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        if (FP4) {
+          const int e = 2 * k + (lane >> 4), l16 = lane & 15;
+          const uint32_t sx = __shfl_sync(0xffffffffu, sc.x, 4 * e + (l16 >> 2));
+          const uint32_t sy = __shfl_sync(0xffffffffu, sc.y, 4 * e + (l16 >> 2));
+          const uint32_t two = ((l16 & 2) ? sy : sx) >> (16 * (l16 & 1));
+          const __half2 sa = pg_fp4_scale(two & 0xFF), sb = pg_fp4_scale((two >> 8) & 0xFF);
+          uint4 c[4] = {pg_decode_fp4(r[k].x, sa), pg_decode_fp4(r[k].y, sa), pg_decode_fp4(r[k].z, sb),
+                        pg_decode_fp4(r[k].w, sb)};
+          const int kb = l16 >> 1;
+          uint8_t* blk = kt + kb * kPgKVBlk;
+          const int row = 8 * wq + e;
+          // the four chunks in an order by block, so that 8 lanes' stores
+          // meet 8 different 16-byte columns
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int cc = m ^ (kb & 3);
+            const uint4 v = cc == 0 ? c[0] : cc == 1 ? c[1] : cc == 2 ? c[2] : c[3];
+            *reinterpret_cast<uint4*>(blk + sw128_offset_h(row, 32 * (l16 & 1) + 8 * cc)) = v;
+          }
+        } else {
+          const uint32_t sx = __shfl_sync(0xffffffffu, sc.x, 4 * k + (lane >> 3));
+          const int ex = (int)((sx >> (8 * ((lane >> 1) & 3))) & 0xFF);
+          uint4 c0, c1;
+          pg_decode_fp8(r[k], ex, c0, c1);
+          const int kb = lane >> 2, row = 8 * wq + k, f = kb & 1;
+          uint8_t* blk = kt + kb * kPgKVBlk;
+          *reinterpret_cast<uint4*>(blk + sw128_offset_h(row, 16 * (lane & 3) + 8 * f)) = f ? c1 : c0;
+          *reinterpret_cast<uint4*>(blk + sw128_offset_h(row, 16 * (lane & 3) + 8 * (f ^ 1))) = f ? c0 : c1;
+        }
+        r[k] = load_word(nptr, k);
+      }
+      if (lane == 0) reinterpret_cast<uint8_t*>(S.valid)[8 * bi + wq] = (uint8_t)vb;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kv_full + bi);
+      sc = scn;
+      vb = vbn;
+      dc.advance(a);
+    }
+  } else {
+    // ------------------------------------------------------ softmax, output
+    const int rr = 32 * (warp & 1) + lane;     // row of the item
+    const int part = warp >> 1;                // entry half
+    const uint32_t trow = tbase + ((uint32_t)(32 * warp) << 16);
+    const float sc = p.scale_log2;
+    PgWalk w;
+    uint32_t t = 0, seg = 0;
+    bool ok = true;
+    int64_t meta_row0 = 0;
+    int meta_rows = 0, meta_cont = 0, meta_done = 0;
+    for (bool go = w.begin(a, S.start); go; go = w.next(a)) {
+      const int nt = w.tiles();
+      const int n_rows = w.s.n * a.H - w.j * kPgRows;
+      const int ri = w.j * kPgRows + rr;
+      // positions this row sees: (lo, hi]; none for rows past the sequence
+      const int hi = rr < n_rows ? w.s.kv - w.s.n + ri / a.H : -1;
+      const int lo = a.window && hi >= a.window ? hi - a.window : -1;
+      float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's entry half
+      for (int i = 0; i < nt; ++i, ++t) {
+        const uint32_t bi = t & 1u;
+        const int kb = w.k0 + (w.off + i) * kPgE + 32 * part;
+        // a failed wait leaves `ok` false and skips the later waits; every
+        // warp still passes the group's barriers once per tile
+        ok = ok && pg_wait_warp(kv_full + bi, (t >> 1) & 1u, kErrWaitTmaFull);
+        uint32_t mask = S.valid[2 * bi + part];
+        const int nh = hi - kb + 1, nl = lo - kb + 1;        // entries [nl, nh) of this half
+        mask &= nh >= 32 ? 0xffffffffu : nh <= 0 ? 0u : (1u << nh) - 1u;
+        mask &= nl <= 0 ? 0xffffffffu : nl >= 32 ? 0u : ~((1u << nl) - 1u);
+        ok = ok && pg_wait_warp(s_full, t & 1u, kErrWaitAccFull);
+        tc_fence_after();
+        uint32_t sv[32];
+        tmem_ld32(trow + kPgSCol + 32 * part, sv);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
+        float mt = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) mt = fmaxf(mt, ((mask >> k) & 1u) ? __uint_as_float(sv[k]) : -INFINITY);
+        if (mt != -INFINITY) mt *= sc;
+        S.mx[(2 * bi + part) * 64 + rr] = mt;
+        uint32_t over;
+        asm volatile("{\n .reg .pred q, r;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred r, 1, 128, q;\n selp.u32 %0, 1, 0, r;\n}"
+                     : "=r"(over) : "r"(mt > m_run + kPgRescale ? 1u : 0u) : "memory");
+        if (over) {
+          const float mm = fmaxf(mt, S.mx[(2 * bi + (part ^ 1)) * 64 + rr]);
+          float alpha = 1.f;
+          if (mm > m_run + kPgRescale) {
+            alpha = m_run == -INFINITY ? 0.f : pg_ex2(m_run - mm);
+            m_run = mm;
+            l_run *= alpha;
+          }
+          if (i > 0) {
+            if (part == 0) S.alpha[rr] = alpha;
+            named_bar(1, 128);
+            ok = ok && pg_wait_warp(o_done, (t - 1) & 1u, kErrWaitAccFull);
+            tc_fence_after();
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {      // 16 rows at a time
+              float al[16];
+#pragma unroll
+              for (int cc = 0; cc < 16; ++cc) al[cc] = S.alpha[16 * k + cc];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t ta = trow + kPgOCol + 64 * c + 16 * k;
+                uint32_t o[16];
+                tmem_ld16(ta, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int cc = 0; cc < 16; ++cc) o[cc] = __float_as_uint(__uint_as_float(o[cc]) * al[cc]);
+                tmem_st16(ta, o);
+              }
+            }
+            tmem_wait_st();
+          }
+        }
+        // the P buffer is free once the PV two tiles back has retired
+        if (t >= 2) ok = ok && pg_wait_warp(kv_free + bi, ((t >> 1) - 1) & 1u, kErrWaitSmemEmpty);
+        const float mref = m_run - kPgPExp;
+        float ls = 0.f;
+        uint8_t* pt = S.p + bi * kPgPBytes;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int e0 = 8 * c + 2 * k;
+            const float x0 = ((mask >> e0) & 1u) ? pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref)) : 0.f;
+            const float x1 = ((mask >> (e0 + 1)) & 1u) ? pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref)) : 0.f;
+            ls += x0 + x1;
+            o[k] = pg_h2u(__floats2half2_rn(x0, x1));
+          }
+          *reinterpret_cast<uint4*>(pt + sw128_offset_h(rr, 32 * part + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        l_run += ls;
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + bi);
+      }
+      // ------------------------------------------------------------ output
+      const bool whole = w.take == w.units;
+      S.lx[64 * part + rr] = l_run;
+      named_bar(1, 128);
+      const int64_t orow = (int64_t)w.s.row0 * a.H + w.j * kPgRows;
+      const int slot = 2 * blockIdx.x + (w.off > 0 ? 0 : 1);
+      if (part == 0) {
+        float l = l_run + S.lx[64 + rr];
+        if (whole) {
+          const float m0 = m_run - kPgPExp;
+          float scl, M = m0, L = l;
+          if (a.sink) {
+            const float s0 = rr < n_rows ? a.sink[ri - ri / a.H * a.H] * kPgLog2e : -INFINITY;
+            M = fmaxf(m0, s0);
+            const float f = l > 0.f ? exp2f(m0 - M) : 0.f;
+            L = l * f + (s0 == -INFINITY ? 0.f : exp2f(s0 - M));
+            scl = l > 0.f ? p.out_scale * f / L : 0.f;
+          } else {
+            scl = l > 0.f ? p.out_scale / l : 0.f;
+          }
+          if (a.lse && rr < n_rows) a.lse[orow + rr] = L > 0.f ? (M + log2f(L)) * kPgLn2 : -INFINITY;
+          S.scl[rr] = scl;
+        } else {
+          p.part_ml[slot * 64 + rr] = make_float2(m_run, l);
+        }
+      }
+      named_bar(1, 128);
+      // every PV of the item.  Not o_done: a parity wait cannot tell phases two
+      // apart, and the last two PVs may both be out
+      if (nt > 0) ok = ok && pg_wait_warp(acc_done, seg++ & 1u, kErrWaitAccFull);
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        const int d = pg_channel<FP4>(128 * c + 32 * warp + lane);
+        uint32_t o[64];
+        if (nt > 0 && ok) {
+          tmem_ld64(trow + kPgOCol + 64 * c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) o[k] = 0u;
+        }
+        if (whole) {
+          if (a.rope_cs && d >= kRopeStart) {          // whole warps: 32 channels from 448 or 480
+#pragma unroll
+            for (int k = 0; k < 64; ++k) {
+              const float v = __uint_as_float(o[k]);
+              const float u = __shfl_xor_sync(0xffffffffu, v, 2);   // channel d ^ 1
+              const int tok = w.s.row0 + (w.j * kPgRows + min(k, n_rows - 1)) / a.H;
+              const float2 cs = *reinterpret_cast<const float2*>(a.rope_cs + (int64_t)tok * 64 + ((d - kRopeStart) & ~1));
+              o[k] = __float_as_uint((d & 1) ? v * cs.x - u * cs.y : v * cs.x + u * cs.y);
+            }
+          }
+          // rows k, k + 1: the lane of the even channel stores row k's pair of
+          // channels, the lane of the odd one row k + 1's
+          __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + orow * kD + (d & ~1);
+          const int odd = d & 1;
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            const float v0 = __uint_as_float(o[k]) * S.scl[k], v1 = __uint_as_float(o[k + 1]) * S.scl[k + 1];
+            const float u = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 2);
+            if (k + odd < n_rows)
+              *reinterpret_cast<__nv_bfloat162*>(ob + (int64_t)(k + odd) * kD) =
+                  odd ? __floats2bfloat162_rn(u, v1) : __floats2bfloat162_rn(v0, u);
+          }
+        } else {
+          float* po = p.part_o + (int64_t)slot * (64 * kD) + d;
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (k < n_rows) po[k * kD] = __uint_as_float(o[k]);
+        }
+      }
+      tc_fence_before();
+      if (!whole) {
+        if (w.off > 0) {
+          meta_cont = 1;
+          meta_done = w.off + w.take == w.units;
+        } else {
+          meta_rows = min(n_rows, kPgRows);
+          meta_row0 = orow;
+        }
+      }
+    }
+    if (tid == 0) p.meta[blockIdx.x] = PgMeta{meta_row0, meta_rows, meta_cont, meta_done, 0};
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPgWarpS) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kPgTmemCols);
+  }
+}
+
+// Joins the partials of the items that several CTAs share.  CTA (i, r): row r
+// of the item that CTA i of the attention began and did not finish; its
+// partials are slot 2i + 1 and then slot 2k of k = i + 1, i + 2, ... up to
+// the CTA that ends the item, added in that order.
+__global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PgParams p, int n_ctas) {
+  pdl_enter();
+  const csa_paged_attn_args& a = p.a;
+  const int i = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31;
+  const PgMeta me = p.meta[i];
+  if (row >= me.rows) return;
+  int n = 1;                                   // partials
+  for (int k0 = i + 1; k0 < n_ctas; k0 += 32) {
+    const uint32_t end = __ballot_sync(0xffffffffu, k0 + lane < n_ctas && p.meta[k0 + lane].cont && p.meta[k0 + lane].done);
+    if (end) {
+      n = k0 - i + __ffs(end);
+      break;
+    }
+    n = min(k0 + 32, n_ctas) - i;
+  }
+  auto slot = [&](int s) { return (int64_t)(s == 0 ? 2 * i + 1 : 2 * (i + s)); };
+  const int64_t orow = me.row0 + row;
+  const int head = (int)(orow % a.H);
+  const float s0 = a.sink ? a.sink[head] * kPgLog2e : -INFINITY;
+  float M = -INFINITY;
+  for (int s = lane; s < n; s += 32) M = fmaxf(M, p.part_ml[slot(s) * 64 + row].x);
+  M = warp_max(M);
+  M = fmaxf(M - kPgPExp, s0);
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* po = p.part_o + (int64_t)row * kD + 4 * threadIdx.x;
+  for (int sb = 0; sb < n; sb += 32) {
+    float wt = 0.f;
+    if (sb + lane < n) {
+      const float2 ml = p.part_ml[slot(sb + lane) * 64 + row];
+      wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - kPgPExp - M);
+      L += wt * ml.y;
+    }
+    const int m = min(32, n - sb);
+#pragma unroll 8
+    for (int s = 0; s < m; ++s) {
+      const float ws = __shfl_sync(0xffffffffu, wt, s);
+      const float4 v = *reinterpret_cast<const float4*>(po + slot(sb + s) * (64 * kD));
+      acc.x += ws * v.x; acc.y += ws * v.y; acc.z += ws * v.z; acc.w += ws * v.w;
+    }
+  }
+  L = warp_sum(L);
+  const bool any = L > 0.f;
+  if (s0 != -INFINITY) L += exp2f(s0 - M);
+  const float f = any ? p.out_scale / L : 0.f;
+  if (threadIdx.x == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kPgLn2 : -INFINITY;
+  const float* cs = a.rope_cs ? a.rope_cs + orow / a.H * 64 : nullptr;
+  store_out4(a.out, true, orow * kD + 4 * threadIdx.x,
+             rope_out4(make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f), cs, 4 * threadIdx.x));
+}
+
+// CTAs of a call: one per SM, fewer when the call cannot have that many units.
+static int pg_grid(const csa_paged_attn_args* a) {
+  const int64_t items = (a->n_rows * a->H + kPgRows - 1) / kPgRows + a->kv.B;
+  const int64_t tiles = ((int64_t)a->kv.max_pages * a->kv.page_size + kPgE - 1) / kPgE;
+  return items * tiles < kNumSMs ? (int)(items * tiles) : kNumSMs;
+}
+static size_t pg_al256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+size_t paged_attn_ws_bytes(const csa_paged_attn_args* a) {
+  const size_t g = (size_t)pg_grid(a);
+  return pg_al256(g * sizeof(PgMeta)) + pg_al256(g * 2 * 64 * sizeof(float2)) + g * 2 * 64 * kD * sizeof(float);
+}
+
+cudaError_t launch_paged_attn(const csa_paged_attn_args* a, void* ws, cudaStream_t stream) {
+  const bool fp4 = a->kv.fmt == CSA_FMT_FP4_E2M1_E4M3X16;
+  static SmemAttrOnce attr4, attr8;
+  const cudaError_t ea = fp4 ? attr4.set(paged_attn_kernel<true>, kPgSmemBytes) : attr8.set(paged_attn_kernel<false>, kPgSmemBytes);
+  if (ea != cudaSuccess) return ea;
+  const int g = pg_grid(a);
+  PgParams p;
+  p.a = *a;
+  // FP4 entries are staged times 2^-7
+  p.scale_log2 = a->softmax_scale * kPgLog2e * (fp4 ? 128.f : 1.f);
+  p.out_scale = fp4 ? 128.f : 1.f;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.meta = reinterpret_cast<PgMeta*>(w);
+  w += pg_al256((size_t)g * sizeof(PgMeta));
+  p.part_ml = reinterpret_cast<float2*>(w);
+  w += pg_al256((size_t)g * 2 * 64 * sizeof(float2));
+  p.part_o = reinterpret_cast<float*>(w);
+  {
+    ProfScope ps(stream, "paged_attn");
+    if (fp4) launch_k(paged_attn_kernel<true>, dim3(g), dim3(kPgThreads), kPgSmemBytes, stream, p);
+    else launch_k(paged_attn_kernel<false>, dim3(g), dim3(kPgThreads), kPgSmemBytes, stream, p);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  {
+    ProfScope ps(stream, "paged_attn_combine");
+    launch_k(paged_attn_combine_kernel, dim3(g, 64), dim3(128), 0, stream, p, g);
+  }
+  note_launches(2);
+  return cudaGetLastError();
+}
+
+int read_pg_error(bool clear) {
+  int v = 0;
+  cudaMemcpyFromSymbol(&v, g_pg_error, sizeof(int));
+  if (clear && v) {
+    int z = 0;
+    cudaMemcpyToSymbol(g_pg_error, &z, sizeof(int));
+  }
+  return v;
+}
+
+}  // namespace csa

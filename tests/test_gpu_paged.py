@@ -1,0 +1,463 @@
+"""GPU parity of the paged cache: append (csa_paged_append) and attention of
+chunks of new tokens (csa_paged_attn) against float64.
+
+Attention tolerance per element, with A = sum_e w_e |x_e| and
+Z = max_e scale * sum_d |q_d x_ed|:
+  * the weights' rounding to fp16: 2^-11 of each, A 2^-11 in all; where the
+    weight is an fp16 subnormal, half of 2^-24 instead, absolute, on a scale
+    where the largest weight (<= 1 of the sum) is at least 2^6: 2^-31 for each
+    entry, 2^-31 sum_e |x_e| in all;
+  * the logits' fp32 accumulation (512 products and the tensor core's own
+    alignment, at most 2^-18 of the sum of magnitudes) and the exp2, which
+    change weights by 2 * (2^-18 Z + 2^-20) relative;
+  * the output's rounding to bf16: 2^-8 |o|;
+  * rotated queries are rounded to fp16: 2^-11 of their share of Z, counted on
+    the whole of it.
+lse: twice the logits' bound plus 2^-20 (1 + |lse|).
+"""
+import numpy as np
+import pytest
+
+from oracle import rope as orope
+from oracle.paged import attend, entry_of, gather, rms_norm, row_positions
+from oracle.quant import fp4_dequant_rows, fp4_quant_rows, fp8_window_dequant_rows, fp8_window_quant_rows
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+ENTRY = {"fp8": 528, "fp4": 288}
+
+
+@pytest.fixture(scope="module")
+def csa():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import indexer_selected_sparse_csa2_b200 as m
+    assert m.device_status() == 0
+    yield m
+    torch.cuda.synchronize()
+    assert m.device_status() == 0
+
+
+def _encode(x, fmt):
+    return (fp8_window_quant_rows if fmt == "fp8" else fp4_quant_rows)(x)
+
+
+class Batch:
+    """A paged cache and new tokens, on the host and on the device.
+    lens: [(new tokens, cache length)]."""
+
+    def __init__(self, seed, lens, H, fmt="fp8", page=16, q_gain=2.0, tail_rows=0, spread=1.0):
+        rng = np.random.default_rng(seed)
+        self.lens, self.H, self.fmt, self.page = lens, H, fmt, page
+        need = [max(1, -(-T // page)) for _, T in lens]
+        self.n_pages = sum(need) + 2
+        ids = rng.permutation(self.n_pages).astype(np.int32)
+        self.table = np.full((len(lens), max(need) + 1), -1, dtype=np.int32)
+        at = 0
+        # bytes that decode to the largest magnitudes wherever nothing was written
+        self.pages = np.full((self.n_pages, page, ENTRY[fmt]), 0x7E, dtype=np.uint8)
+        for b, (n, T) in enumerate(lens):
+            self.table[b, :need[b]] = ids[at:at + need[b]]
+            at += need[b]
+            if T > 0:
+                e = _encode((rng.standard_normal((T, 512)) * spread).astype(np.float32), fmt)
+                for p in range(0, T, page):
+                    k = min(page, T - p)
+                    self.pages[self.table[b, p // page], :k] = e[p:p + k]
+        self.cu = np.concatenate([[0], np.cumsum([n for n, _ in lens])]).astype(np.int32)
+        self.kv = np.array([T for _, T in lens], dtype=np.int32)
+        self.rows = int(self.cu[-1]) + tail_rows
+        self.q = torch.from_numpy((q_gain * rng.standard_normal((max(1, self.rows), H, 512))).astype(np.float32)).to(torch.bfloat16)
+        self.sink = rng.standard_normal(H).astype(np.float32)
+        self.cs = np.stack([orope.rope_angles(i) for i in range(max(1, self.rows))])
+
+    def device(self, csa):
+        dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+        self.d = dict(pages=dev(self.pages), block_table=dev(self.table), cu_q=dev(self.cu), kv_len=dev(self.kv))
+        return csa.paged_kv(**self.d)
+
+    def want(self, window=0, sink=None, rope=False, scale=512 ** -0.5):
+        n = int(self.cu[-1])
+        out, mass = np.zeros((n, self.H, 512)), np.zeros((n, self.H, 512))
+        lse, size, total = np.zeros((n, self.H)), np.zeros((n, self.H)), np.zeros((n, 1, 512))
+        pos = np.array([p for _, p in row_positions(self.cu, self.kv)], dtype=np.int64)
+        q = self.q[:n].double().numpy()
+        for b in range(len(self.lens)):
+            i, j = self.cu[b], self.cu[b + 1]
+            if i == j:
+                continue
+            kp, X = gather(self.pages, self.table, b, range(0, max(0, int(self.kv[b]))))
+            qq = q[i:j]
+            if rope:
+                qq = np.stack([orope.rotate(qq[t], self.cs[i + t]) for t in range(j - i)])
+            out[i:j], lse[i:j], mass[i:j], size[i:j], total[i:j] = attend(qq, pos[i:j], kp, X, scale, window, sink)
+        if rope:
+            out = np.stack([orope.rotate(out[t], self.cs[t], inverse=True) for t in range(n)]) if n else out
+            for m in (mass, total):                # a rotated pair's error stays within the pair's sum
+                both = m[..., 448::2] + m[..., 449::2]
+                m[..., 448::2] = m[..., 449::2] = both
+        return out, lse, mass, size, total
+
+
+def _check(got, got_lse, want, rope=False):
+    out, lse, mass, size, total = want
+    n = out.shape[0]
+    g = got[:n].double().cpu().numpy()
+    dl = 2.0 ** -18 * size + 2.0 ** -20 + (2.0 ** -11 * size if rope else 0)
+    tol = 2.0 ** -11 * mass + 2.0 ** -31 * total + 2 * dl[..., None] * mass + 2.0 ** -8 * np.abs(out) + 1e-30
+    bad = np.abs(g - out) > tol
+    assert not bad.any(), (int(bad.sum()), float((np.abs(g - out) / tol).max()), np.argwhere(bad)[:4].tolist())
+    if got_lse is not None:
+        l = got_lse[:n].double().cpu().numpy()
+        assert np.array_equal(np.isneginf(l), np.isneginf(lse))
+        fin = np.isfinite(lse)
+        assert np.all(np.abs(l[fin] - lse[fin]) <= 2 * dl[fin] + 2.0 ** -20 * (1 + np.abs(lse[fin])))
+
+
+def _run(csa, B, kv, window=0, sink=None, rope=False, scale=512 ** -0.5, q=None, stream=None, ws=None):
+    q = B.q.cuda() if q is None else q
+    out = torch.full((q.shape[0], B.H, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((q.shape[0], B.H), 3.0, device="cuda")
+    a = csa.paged_attn_args(q=q, kv=kv, out=out, lse=lse, softmax_scale=scale, window=window,
+                            sink=None if sink is None else torch.from_numpy(sink).cuda(),
+                            rope_cs=torch.from_numpy(B.cs).cuda() if rope else None)
+    if ws is None:                                   # whatever the workspace holds
+        ws = torch.full((csa.csa_paged_attn_workspace_size(a),), 0xFF, dtype=torch.uint8, device="cuda")
+    csa.csa_paged_attn(a, workspace=ws)
+    torch.cuda.synchronize()
+    assert csa.device_status() == 0
+    return out, lse
+
+
+SMALL = [
+    # lens, H, fmt, page, window, sink
+    ([(1, 1)], 1, "fp8", 16, 0, False),
+    ([(1, 64)], 64, "fp8", 64, 0, False),
+    ([(1, 65)], 64, "fp4", 16, 0, True),
+    ([(3, 3), (1, 17), (0, 40), (5, 200)], 16, "fp8", 7, 0, True),
+    ([(3, 3), (1, 17), (0, 40), (5, 200)], 16, "fp4", 100, 0, False),
+    ([(70, 70), (2, 130)], 3, "fp8", 16, 0, False),
+    ([(33, 300)], 128, "fp8", 32, 0, True),
+    ([(20, 150), (9, 64)], 24, "fp4", 1, 0, True),
+    ([(40, 400), (1, 129), (7, 7)], 64, "fp8", 64, 128, True),
+    ([(40, 400), (1, 129), (7, 7)], 64, "fp4", 64, 1, False),
+    ([(90, 90)], 8, "fp8", 256, 33, False),
+    ([(1, 5000)], 64, "fp8", 64, 0, True),
+    ([(2, 3001), (1, 1), (1, 900)], 40, "fp4", 64, 0, False),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SMALL)))
+def test_attention(csa, case):
+    lens, H, fmt, page, window, sink = SMALL[case]
+    B = Batch(100 + case, lens, H, fmt, page)
+    s = B.sink if sink else None
+    out, lse = _run(csa, B, B.device(csa), window, s)
+    _check(out, lse, B.want(window, s))
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("scale", [0.0, 1e-3, 1.0])
+def test_softmax_scales(csa, fmt, scale):
+    B = Batch(7, [(5, 300), (1, 70)], 16, fmt, 32)
+    out, lse = _run(csa, B, B.device(csa), scale=scale)
+    _check(out, lse, B.want(scale=scale))
+
+
+def test_running_max_moves_late_and_early(csa):
+    """Key norms that grow and fall along the cache: the rescaling path."""
+    for order in (1, -1):
+        B = Batch(8, [(4, 900)], 32, "fp8", 16)
+        gain = np.linspace(0.05, 6.0, 900)[::order]
+        rng = np.random.default_rng(3)
+        e = _encode((rng.standard_normal((900, 512)) * gain[:, None]).astype(np.float32), "fp8")
+        for p in range(0, 900, 16):
+            k = min(16, 900 - p)
+            B.pages[B.table[0, p // 16], :k] = e[p:p + k]
+        out, lse = _run(csa, B, B.device(csa))
+        _check(out, lse, B.want())
+
+
+def test_block_exponents_far_from_one(csa):
+    """FP8 blocks whose scale is outside fp16's powers of two, next to
+    ordinary ones, and every E4M3 code."""
+    B = Batch(9, [(3, 200)], 16, "fp8", 16)
+    flat = B.pages.reshape(-1, 528)
+    rng = np.random.default_rng(4)
+    for p in range(200):
+        row = flat[B.table[0, p // 16] * 16 + p % 16]
+        row[:512] = rng.permutation(np.tile([c for c in range(256) if c & 0x7F != 0x7F], 3))[:512]
+        row[512:] = rng.integers(90, 124, 16)
+    out, lse = _run(csa, B, B.device(csa), scale=0.02)
+    # decoded values below 2^-14 are rounded to fp16's 2^-24 grid: 2^-25 on a
+    # value, and through the logits 0.02 * sum |q| 2^-25
+    want = B.want(scale=0.02)
+    size = want[3] + 0.02 * 2.0 ** -7 * np.abs(B.q.double().numpy()).sum(-1)
+    _check(out, lse, (want[0], want[1], want[2] + 2.0 ** -13, size, want[4]))
+
+
+def test_rows_that_see_nothing(csa):
+    """Fewer cached tokens than new ones (negative positions), an empty cache,
+    pages that are missing: zero rows, lse = sink or -inf."""
+    B = Batch(10, [(6, 6), (4, 4), (3, 100)], 16, "fp8", 16)
+    B.kv = np.array([2, 0, 100], dtype=np.int32)
+    B.table[2, :] = -1
+    B.table[2, 1] = B.n_pages + 3
+    kv = B.device(csa)
+    for sink in (None, B.sink, np.full(16, -np.inf, dtype=np.float32)):
+        out, lse = _run(csa, B, kv, sink=sink)
+        want = B.want(sink=sink)
+        _check(out, lse, want)
+        assert torch.all(out[:4] == 0) and torch.all(out[6:] == 0)
+        ref = torch.full((7, 16), -np.inf) if sink is None else torch.from_numpy(sink).expand(7, 16)
+        assert torch.allclose(lse[6:].cpu(), ref, rtol=1e-6)
+
+
+def test_missing_pages_are_left_out(csa):
+    B = Batch(11, [(5, 500), (2, 90)], 32, "fp4", 16)
+    B.table[0, 3] = -1
+    B.table[0, 10] = B.n_pages
+    B.table[0, 11] = -2 ** 31
+    B.table[0, 12] = 2 ** 31 - 1
+    B.table[1, 5] = -7                              # the newest tokens' page
+    out, lse = _run(csa, B, B.device(csa))
+    _check(out, lse, B.want())
+
+
+def test_cache_longer_than_its_table(csa):
+    """kv_len past the table: positions without a page hold no entry."""
+    B = Batch(12, [(3, 64)], 16, "fp8", 16)
+    B.table = B.table[:, :4].copy()
+    B.kv = np.array([100], dtype=np.int32)
+    out, lse = _run(csa, B, B.device(csa))
+    _check(out, lse, B.want())
+    B.kv = np.array([2 ** 31 - 1], dtype=np.int32)
+    out, lse = _run(csa, B, B.device(csa))
+    kp, X = gather(B.pages, B.table, 0, range(64))
+    _check(out, lse, attend(B.q.double().numpy(), np.full(3, 10 ** 9), kp, X, 512 ** -0.5))
+
+
+def test_rows_behind_the_last_sequence_stay(csa):
+    B = Batch(13, [(5, 50), (0, 9), (2, 33)], 16, "fp8", 16, tail_rows=9)
+    out, lse = _run(csa, B, B.device(csa))
+    _check(out, lse, B.want())
+    assert torch.all(out[7:] == 3.0) and torch.all(lse[7:] == 3.0)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_rope(csa, fmt):
+    B = Batch(14, [(20, 90), (1, 700), (3, 3)], 16, fmt, 16)
+    out, lse = _run(csa, B, B.device(csa), rope=True, sink=B.sink)
+    _check(out, lse, B.want(rope=True, sink=B.sink), rope=True)
+
+
+def test_strided_queries_pages_and_entries(csa):
+    B = Batch(15, [(9, 140), (1, 31)], 24, "fp8", 16)
+    B.device(csa)
+    big = torch.full((B.n_pages, 18, 560), 0x7E, dtype=torch.uint8, device="cuda")
+    pages = big[:, 1:17, 16:544]
+    pages.copy_(B.d["pages"])
+    table = torch.full((2, 40), -1, dtype=torch.int32, device="cuda")
+    table[:, :B.table.shape[1]] = B.d["block_table"]
+    kv = csa.paged_kv(pages=pages, block_table=table[:, :B.table.shape[1]], cu_q=B.d["cu_q"], kv_len=B.d["kv_len"])
+    q = torch.full((B.rows, 24, 576), 1e4, dtype=torch.bfloat16, device="cuda")
+    q[..., 32:544] = B.q.cuda()
+    out, lse = _run(csa, B, kv, q=q[..., 32:544])
+    _check(out, lse, B.want())
+    qt = B.q.cuda().transpose(0, 1).contiguous().transpose(0, 1)        # heads outermost
+    out2, lse2 = _run(csa, B, kv, q=qt)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_page_offsets_past_32_bits(csa):
+    B = Batch(16, [(2, 40)], 16, "fp8", 16)
+    B.device(csa)
+    stride = (5 << 30) // 2
+    buf = torch.zeros(2 * stride + 16 * 528 + 64, dtype=torch.uint8, device="cuda")
+    pages = buf.as_strided((3, 16, 528), (stride, 528, 1))
+    order = B.table[0, :3]
+    for i in range(3):
+        pages[i] = B.d["pages"][int(order[i])]
+    table = torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda")
+    kv = csa.paged_kv(pages=pages, block_table=table, cu_q=B.d["cu_q"], kv_len=B.d["kv_len"])
+    out, lse = _run(csa, B, kv)
+    _check(out, lse, B.want())
+    del buf, pages
+
+
+def test_same_bits_on_every_run(csa):
+    B = Batch(17, [(1, 4000), (30, 500), (1, 2)], 64, "fp8", 64)
+    kv = B.device(csa)
+    first = _run(csa, B, kv)
+    for _ in range(3):
+        again = _run(csa, B, kv)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+def test_two_streams_at_once(csa):
+    P = [Batch(18, [(1, 3000)], 64, "fp8", 64), Batch(19, [(60, 400), (1, 9)], 32, "fp4", 16)]
+    kvs = [b.device(csa) for b in P]
+    alone = [_run(csa, b, k) for b, k in zip(P, kvs)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    res = []
+    for b, k in zip(P, kvs):
+        q = b.q.cuda()
+        out, lse = torch.empty(b.rows, b.H, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(b.rows, b.H, device="cuda")
+        a = csa.paged_attn_args(q=q, kv=k, out=out, lse=lse, softmax_scale=512 ** -0.5)
+        res.append((a, torch.empty(csa.csa_paged_attn_workspace_size(a), dtype=torch.uint8, device="cuda"), out, lse))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, (a, ws, _, _) in zip(streams, res):
+            csa.csa_paged_attn(a, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for (_, _, out, lse), (o, l) in zip(res, alone):
+        assert torch.equal(out, o) and torch.equal(lse, l)
+
+
+def test_graph_replay_follows_the_lengths(csa):
+    B = Batch(20, [(4, 300), (4, 200)], 16, "fp8", 16, tail_rows=4)
+    kv = B.device(csa)
+    q = B.q.cuda()
+    out, lse = torch.zeros(B.rows, 16, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(B.rows, 16, device="cuda")
+    a = csa.paged_attn_args(q=q, kv=kv, out=out, lse=lse, softmax_scale=512 ** -0.5)
+    ws = torch.empty(csa.csa_paged_attn_workspace_size(a), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        csa.csa_paged_attn(a, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        csa.csa_paged_attn(a, workspace=ws)
+    for lens, cu in (([300, 200], [0, 4, 8]), ([17, 200], [0, 9, 12]), ([250, 3], [0, 1, 3])):
+        B.cu, B.kv = np.array(cu, dtype=np.int32), np.array(lens, dtype=np.int32)
+        B.d["cu_q"].copy_(torch.from_numpy(B.cu))
+        B.d["kv_len"].copy_(torch.from_numpy(B.kv))
+        g.replay()
+        torch.cuda.synchronize()
+        _check(out, lse, B.want())
+
+
+# -------------------------------------------------------------------- append
+def _append(csa, B, src, n_rows=None, **kw):
+    kv = B.device(csa)
+    csa.csa_paged_append(csa.paged_append_args(src=src, kv=kv, **kw))
+    torch.cuda.synchronize()
+    return B.d["pages"].cpu().numpy()
+
+
+APPENDS = [([(1, 1)], 16), ([(3, 50), (0, 7), (1, 16), (20, 20)], 16), ([(1, 100)] * 40, 7), ([(300, 1000), (5, 5)], 64),
+           ([(1, 3)] * 1200, 16)]
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("case", range(len(APPENDS)))
+def test_append_without_norm_is_the_encoder(csa, fmt, dtype, case):
+    """Bit for bit the entries of csa_quant_kv's definition, and nothing else touched."""
+    lens, page = APPENDS[case]
+    B = Batch(30 + case, lens, 1, fmt, page)
+    x = torch.from_numpy(np.random.default_rng(case).standard_normal((B.rows + 3, 512)).astype(np.float32) * 5).to(getattr(torch, dtype)).cuda()
+    want = B.pages.copy()
+    enc = _encode(x.float().cpu().numpy(), fmt)
+    for r, (b, p) in enumerate(row_positions(B.cu, B.kv)):
+        want[entry_of(B.table, page, B.n_pages, b, p)] = enc[r]
+    assert np.array_equal(_append(csa, B, x), want)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("weight", [False, True])
+@pytest.mark.parametrize("rope", [False, True])
+def test_append_norm_and_rope(csa, fmt, weight, rope):
+    """Decoded entries within half a step of the exact normed and rotated row:
+    FP8 2^-4 relative or 2^-10 of the block's scale; FP4 half the E2M1 step at
+    the value (at most 1/4 of it, or 1/4 of the scale), plus the clipping that
+    a scale rounded down by 2^-4 causes; 2^-17 for the fp32 arithmetic."""
+    lens = [(9, 60), (30, 30), (1, 77)]
+    B = Batch(40, lens, 1, fmt, 16)
+    rng = np.random.default_rng(6)
+    x = torch.from_numpy((rng.standard_normal((B.rows, 512)) * 4).astype(np.float32)).to(torch.bfloat16).cuda()
+    w = (1 + 0.3 * rng.standard_normal(512)).astype(np.float32)
+    pages = _append(csa, B, x, norm=True, eps=1e-5, weight=torch.from_numpy(w).cuda() if weight else None,
+                    rope_cs=torch.from_numpy(B.cs).cuda() if rope else None)
+    _, y = rms_norm(x.double().cpu().numpy(), 1e-5, w if weight else None)
+    if rope:
+        y = np.concatenate([orope.rotate(y[i:i + 1], B.cs[i]) for i in range(B.rows)])
+    raw = np.stack([pages[entry_of(B.table, 16, B.n_pages, b, p)] for b, p in row_positions(B.cu, B.kv)])
+    if fmt == "fp8":
+        got, s = fp8_window_dequant_rows(raw), np.repeat(np.ldexp(1.0, raw[:, 512:].astype(int) - 127), 32, axis=1)
+        tol = np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * s)
+        amax = np.abs(y).reshape(-1, 16, 32).max(2)
+        assert np.all(amax <= 448 * s[:, ::32] * (1 + 2.0 ** -17)) and np.all(amax >= 224 * s[:, ::32] * (1 - 2.0 ** -17))
+    else:
+        got = fp4_dequant_rows(raw)
+        amax = np.repeat(np.abs(y).reshape(-1, 32, 16).max(2), 16, axis=1)
+        s = amax / 6
+        tol = np.maximum(0.25 * s * (1 + 2.0 ** -4), np.minimum(np.abs(y) / 4, s) * (1 + 2.0 ** -4)) + 2.0 ** -4 * np.abs(y)
+    assert np.all(np.abs(got - y) <= tol + 2.0 ** -17 * np.abs(y)), float((np.abs(got - y) - tol).max())
+    # and the rows' neighbours in their pages stay
+    touched = np.zeros(B.pages.shape[:2], dtype=bool)
+    for b, p in row_positions(B.cu, B.kv):
+        touched[entry_of(B.table, 16, B.n_pages, b, p)] = True
+    assert np.array_equal(pages[~touched], B.pages[~touched])
+
+
+def test_append_skips_what_has_no_entry(csa):
+    """Negative positions, missing pages, positions past the table, rows behind
+    the last sequence: nothing is written for them."""
+    B = Batch(41, [(6, 6), (4, 64), (3, 3)], 1, "fp8", 16, tail_rows=5)
+    B.kv = np.array([2, 64, 2 ** 31 - 1], dtype=np.int32)
+    B.table[1, 3] = B.n_pages
+    x = torch.randn(B.rows, 512, device="cuda")
+    want = B.pages.copy()
+    enc = _encode(x.cpu().numpy(), "fp8")
+    for r in (4, 5):
+        want[entry_of(B.table, 16, B.n_pages, 0, r - 4)] = enc[r]
+    assert np.array_equal(_append(csa, B, x), want)
+
+
+# ----------------------------------------------------------------- the chain
+def test_norm_append_attention_as_a_layer_uses_them(csa):
+    """Residual stream -> norm with 8-bit output (decoded as an 8-bit
+    projection would) -> latents and queries -> append -> attention, for three
+    steps: a prompt, a chunk, single tokens; each step's attention against
+    float64 over the cache as the library wrote it."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    dim, H, page = 1024, 16, 16
+    wk, wq = rnd(dim, 512) / 32, rnd(dim, H * 512) / 32
+    wn, wl = 1 + 0.1 * rnd(dim), 1 + 0.1 * rnd(512)
+    pages = torch.zeros(40, page, 528, dtype=torch.uint8, device="cuda")
+    table = torch.randperm(40, generator=g, device="cuda").to(torch.int32).view(2, 20)
+    kv_now = [0, 0]
+    residual = None
+    for step, new in enumerate(([37, 5], [1, 40], [1, 1], [1, 1])):
+        n = sum(new)
+        kv_now = [a + b for a, b in zip(kv_now, new)]
+        cu = torch.tensor([0, new[0], n], dtype=torch.int32, device="cuda")
+        kvl = torch.tensor(kv_now, dtype=torch.int32, device="cuda")
+        x, residual = rnd(n, dim).to(torch.bfloat16), rnd(n, dim).to(torch.bfloat16)
+        codes = torch.empty(n, dim, dtype=torch.uint8, device="cuda")
+        sc = torch.empty(n, dim // 32, dtype=torch.uint8, device="cuda")
+        csa.csa_rms_norm(csa.rms_norm_args(x=x, residual=residual, residual_out=residual, weight=wn, codes=codes, scales=sc))
+        h = codes.view(torch.float8_e4m3fn).float().view(n, -1, 32) * torch.exp2(sc.float() - 127)[:, :, None]
+        h = h.view(n, dim)
+        lat, q = (h @ wk).to(torch.bfloat16), (h @ wq).view(n, H, 512).to(torch.bfloat16)
+        pos = [kv_now[b] - new[b] + t for b in range(2) for t in range(new[b])]
+        cs = torch.from_numpy(np.stack([orope.rope_angles(p) for p in pos]).astype(np.float32)).cuda()
+        kv = csa.paged_kv(pages=pages, block_table=table, cu_q=cu, kv_len=kvl)
+        csa.csa_paged_append(csa.paged_append_args(src=lat, kv=kv, norm=True, weight=wl, rope_cs=cs))
+        out, lse = torch.empty_like(q), torch.empty(n, H, device="cuda")
+        csa.csa_paged_attn(csa.paged_attn_args(q=q, kv=kv, out=out, lse=lse, softmax_scale=512 ** -0.5, rope_cs=cs))
+        torch.cuda.synchronize()
+        B = Batch(0, [(k, t) for k, t in zip(new, kv_now)], H, "fp8", page)
+        B.pages, B.table, B.n_pages, B.q, B.cs = pages.cpu().numpy(), table.cpu().numpy(), 40, q.cpu(), cs.cpu().numpy()
+        _check(out, lse, B.want(rope=True), rope=True)
+        # the newest latents of the cache are the normed, rotated ones
+        _, y = rms_norm(lat.double().cpu().numpy(), 1e-6, wl.double().cpu().numpy())
+        y = np.concatenate([orope.rotate(y[i:i + 1], B.cs[i]) for i in range(n)])
+        raw = np.stack([B.pages[entry_of(B.table, page, 40, b, p)] for b, p in row_positions(B.cu, B.kv)])
+        s = np.repeat(np.ldexp(1.0, raw[:, 512:].astype(int) - 127), 32, axis=1)
+        err = np.abs(fp8_window_dequant_rows(raw) - y)
+        assert np.all(err <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * s) + 2.0 ** -17 * np.abs(y))
