@@ -27,9 +27,8 @@
 // (max, sum, O^T) partials in the workspace, at most two per CTA, which
 // paged_attn_combine joins in CTA order; the result does not depend on timing.
 //
-// Warp roles: 0-3 softmax and output, 4-11 entry loads and decoding, and the
-// staging of Q at the start of an item, 12 issues the S MMAs, 13 the PV MMAs.
-// Entry tiles and P are double buffered; the entries of tile t + 1 are loaded
+// Warp roles: 0-3 staging of Q, softmax and output, 4-11 entry loads and
+// decoding, 12 issues the S MMAs, 13 the PV MMAs.  Entry tiles and P are double buffered; the entries of tile t + 1 are loaded
 // into registers as tile t's are decoded, page table values one tile earlier.
 #include <climits>
 
@@ -123,6 +122,32 @@ CSA_DEV float pg_ex2(float x) {
 // Bounded wait by a whole warp, the same answer in every lane.
 CSA_DEV bool pg_wait_warp(uint64_t* bar, uint32_t parity, int code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_pg_error, code));
+}
+
+// MMAs with descriptors given by their low words (the high words are
+// constants of the layout), so that an unrolled sequence costs one addition
+// per operand; issued by one lane of a warp that runs its loops as a whole.
+constexpr uint32_t kPgDescK = (1024u >> 4) | 1u << 14 | 2u << 29;    // K-major, 128-byte swizzle: high word
+CSA_DEV uint32_t pg_desc_k(uint32_t smem_addr) { return (smem_addr >> 4) | 1u << 16; }
+CSA_DEV uint32_t pg_desc_mn(uint32_t smem_addr, uint32_t lbo) { return (smem_addr >> 4) | (lbo >> 4) << 16; }
+template <bool ACC>
+CSA_DEV void pg_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
+      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kPgDescK), "n"(ACC ? 1 : 0) : "memory");
+}
+template <bool ACC>
+CSA_DEV void pg_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}"
+      ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDescK), "n"(ACC ? 1 : 0) : "memory");
+}
+CSA_DEV bool pg_elect() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+  return e != 0;
 }
 
 // ------------------------------------------------------------- work items --
@@ -338,28 +363,26 @@ CSA_DEV void pg_bf16x8(const uint4& v, float (&f)[8]) {
 // land on subnormals, so every code is exact.
 CSA_DEV uint32_t pg_e4m3_02(uint32_t w) { return ((w << 7) & 0x3F803F80u) | ((w << 8) & 0x80008000u); }
 CSA_DEV uint32_t pg_e4m3_13(uint32_t w) { return ((w >> 1) & 0x3F803F80u) | (w & 0x80008000u); }
-// 16 codes of one FP8 block half -> two 8-channel chunks of fp16 values.
-CSA_DEV void pg_decode_fp8(const uint4& v, int ex, uint4& c0, uint4& c1) {
+// 16 codes of one FP8 block half -> two 8-channel chunks of fp16 values
+// (E4M3 * 2^-8) * f2, f2 = 2^(exponent byte - 119) twice, a power of two that
+// fp16 holds (exponent bytes 105..134), or 0.
+CSA_DEV void pg_decode_fp8(const uint4& v, uint32_t f2, uint4& c0, uint4& c1) {
+  const __half2 f = pg_u2h(f2);
+  c0 = make_uint4(pg_h2u(__hmul2(pg_u2h(pg_e4m3_02(v.x)), f)), pg_h2u(__hmul2(pg_u2h(pg_e4m3_13(v.x)), f)),
+                  pg_h2u(__hmul2(pg_u2h(pg_e4m3_02(v.y)), f)), pg_h2u(__hmul2(pg_u2h(pg_e4m3_13(v.y)), f)));
+  c1 = make_uint4(pg_h2u(__hmul2(pg_u2h(pg_e4m3_02(v.z)), f)), pg_h2u(__hmul2(pg_u2h(pg_e4m3_13(v.z)), f)),
+                  pg_h2u(__hmul2(pg_u2h(pg_e4m3_02(v.w)), f)), pg_h2u(__hmul2(pg_u2h(pg_e4m3_13(v.w)), f)));
+}
+// Any exponent byte: fp32 product, rounded to fp16.
+CSA_DEV void pg_decode_fp8_far(const uint4& v, int ex, uint4& c0, uint4& c1) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t o[8];
-  if (ex >= 105 && ex <= 134) {
-    // (E4M3 * 2^-8) * 2^(ex - 119), a power of two that fp16 holds
-    const uint32_t f = (uint32_t)(ex - 104) << 10;
-    const __half2 f2 = pg_u2h(f | (f << 16));
+  const float f = exp2f((float)(ex - 119));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      o[2 * k] = pg_h2u(__hmul2(pg_u2h(pg_e4m3_02(w[k])), f2));
-      o[2 * k + 1] = pg_h2u(__hmul2(pg_u2h(pg_e4m3_13(w[k])), f2));
-    }
-  } else {
-    // scales far from 1: fp32 product, rounded to fp16
-    const float f = exp2f((float)(ex - 119));
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 a = __half22float2(pg_u2h(pg_e4m3_02(w[k]))), b = __half22float2(pg_u2h(pg_e4m3_13(w[k])));
-      o[2 * k] = pg_h2u(__floats2half2_rn(a.x * f, a.y * f));
-      o[2 * k + 1] = pg_h2u(__floats2half2_rn(b.x * f, b.y * f));
-    }
+  for (int k = 0; k < 4; ++k) {
+    const float2 a = __half22float2(pg_u2h(pg_e4m3_02(w[k]))), b = __half22float2(pg_u2h(pg_e4m3_13(w[k])));
+    o[2 * k] = pg_h2u(__floats2half2_rn(a.x * f, a.y * f));
+    o[2 * k + 1] = pg_h2u(__floats2half2_rn(b.x * f, b.y * f));
   }
   c0 = make_uint4(o[0], o[1], o[2], o[3]);
   c1 = make_uint4(o[4], o[5], o[6], o[7]);
@@ -378,6 +401,78 @@ CSA_DEV uint4 pg_decode_fp4(uint32_t w, __half2 s2) {
 }
 CSA_DEV __half2 pg_fp4_scale(uint32_t code) {   // E4M3 scale * 2^7, twice
   return __hmul2(pg_u2h(pg_e4m3_02(code | (code << 16))), pg_u2h(0x78007800u));
+}
+
+// Stages an item's 64 query rows: channels 0..383 into TMEM lanes 32 warp ..
+// (twice: lanes L and L + 64 hold row L), channels 384..511 into the two
+// shared blocks.  Called by warps 0-3; rows past the sequence are zero.
+template <bool FP4>
+CSA_DEV void pg_stage_q(const csa_paged_attn_args& a, const PgWalk& w, const PgSmem& S, uint32_t trow, int warp, int lane) {
+  const int n_rows = w.s.n * a.H - w.j * kPgRows;          // rows left in the sequence from this item on
+  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q);
+  auto q_row = [&](int rr) -> const __nv_bfloat16* {
+    const int ri = w.j * kPgRows + rr, tok = ri / a.H;
+    return qb + (int64_t)(w.s.row0 + tok) * a.q_row_stride + (int64_t)(ri - tok * a.H) * a.q_head_stride;
+  };
+  {
+    const int rr = 32 * (warp & 1) + lane;
+    const bool on = rr < n_rows;
+    const uint4* src = reinterpret_cast<const uint4*>(q_row(on ? rr : 0));
+#pragma unroll 1
+    for (int u = 0; u < 12; u += 2) {                      // 32 columns: 64 channels
+      uint4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = on ? src[4 * u + k] : make_uint4(0, 0, 0, 0);
+      uint32_t o[2][16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        float f[8];
+        uint32_t ow[4];
+        pg_bf16x8(v[k], f);
+        pg_q_words<FP4>(f, ow);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) o[k >> 2][4 * (k & 3) + m] = ow[m];
+      }
+      tmem_st16(trow + 16u * u, o[0]);
+      tmem_st16(trow + 16u * u + 16, o[1]);
+    }
+  }
+  const int st = 32 * warp + lane;                         // 128 threads
+#pragma unroll 1
+  for (int k0 = 0; k0 < 8; k0 += 4) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int rr = (st >> 4) + 8 * (k0 + k);
+      v[k] = rr < n_rows ? *reinterpret_cast<const uint4*>(q_row(rr) + 384 + 8 * (st & 15)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int rr = (st >> 4) + 8 * (k0 + k), c16 = st & 15;
+      float f[8];
+      pg_bf16x8(v[k], f);
+      if (a.rope_cs && c16 >= 8 && rr < n_rows) {          // channels 448 + 8 (c16 - 8) ..
+        const int tok = w.s.row0 + (w.j * kPgRows + rr) / a.H;
+        const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * (c16 - 8));
+        const float4 ca = cs[0], cb = cs[1];
+        float2 g;
+        g = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = g.x; f[1] = g.y;
+        g = rope_fwd(f[2], f[3], ca.z, ca.w); f[2] = g.x; f[3] = g.y;
+        g = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = g.x; f[5] = g.y;
+        g = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = g.x; f[7] = g.y;
+      }
+      uint32_t ow[4];
+      pg_q_words<FP4>(f, ow);
+      const uint4 o = make_uint4(ow[0], ow[1], ow[2], ow[3]);
+      uint8_t* blk = S.q + (c16 >> 3) * kPgQBlk;
+      *reinterpret_cast<uint4*>(blk + sw128_offset_h(rr, 8 * (c16 & 7))) = o;
+      *reinterpret_cast<uint4*>(blk + sw128_offset_h(rr + 64, 8 * (c16 & 7))) = o;
+    }
+  }
+  tmem_wait_st();
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncwarp();
 }
 
 // A position in the CTA's list of key tiles.
@@ -414,8 +509,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   uint64_t* s_free = S.bars + 5;     // S read by the softmax (4 warp arrivals)
   uint64_t* p_full = S.bars + 6;     // [2] P written, O^T rescaled (4 warp arrivals)
   uint64_t* o_done = S.bars + 8;     // one phase per PV
-  uint64_t* q_full = S.bars + 9;     // an item's Q staged (8 warp arrivals)
-  uint64_t* q_free = S.bars + 10;    // an item's last S done
+  uint64_t* q_full = S.bars + 9;     // an item's Q staged (4 warp arrivals)
   uint64_t* acc_done = S.bars + 11;  // an item's last PV done (one phase per item)
   uint64_t* drain = S.bars + 12;     // [2] all MMAs of an issuer retired (teardown)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -430,8 +524,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     mbar_init(s_full, 1);
     mbar_init(s_free, 4);
     mbar_init(o_done, 1);
-    mbar_init(q_full, kPgDeqWarps);
-    mbar_init(q_free, 1);
+    mbar_init(q_full, 4);
     mbar_init(acc_done, 1);
     fence_mbar_init();
   }
@@ -445,79 +538,85 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 
   if (warp == kPgWarpS) {
     // ------------------------------------------------------------ S issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_make(kFmtF16, kFmtF16, 128, kPgE);
-      const uint32_t qa = smem_u32(S.q), kva = smem_u32(S.kv);
-      PgWalk w;
-      uint32_t t = 0, seg = 0;
-      bool ok = true;
-      for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
-        const int nt = w.tiles();
-        if (nt == 0) continue;
-        ok = mbar_wait(q_full, seg & 1u, &g_pg_error, kErrWaitTmaFull);
-        for (int i = 0; i < nt && ok; ++i, ++t) {
-          const uint32_t bi = t & 1u;
-          ok = mbar_wait(kv_full + bi, (t >> 1) & 1u, &g_pg_error, kErrWaitTmaFull);
-          if (ok && t >= 1) ok = mbar_wait(s_free, (t - 1) & 1u, &g_pg_error, kErrWaitAccEmpty);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t kvt = kva + bi * kPgKVBytes;
+    constexpr uint32_t idesc = idesc_make(kFmtF16, kFmtF16, 128, kPgE);
+    const uint32_t qd = pg_desc_k(smem_u32(S.q)), kvd = pg_desc_k(smem_u32(S.kv));
+    PgWalk w;
+    uint32_t t = 0, seg = 0;
+    bool ok = true;
+    for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
+      const int nt = w.tiles();
+      if (nt == 0) continue;
+      ok = pg_wait_warp(q_full, seg++ & 1u, kErrWaitTmaFull);
+      for (int i = 0; i < nt && ok; ++i, ++t) {
+        const uint32_t bi = t & 1u;
+        ok = pg_wait_warp(kv_full + bi, (t >> 1) & 1u, kErrWaitTmaFull);
+        if (ok && t >= 1) ok = pg_wait_warp(s_free, (t - 1) & 1u, kErrWaitAccEmpty);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t kd = kvd + bi * (kPgKVBytes >> 4);
+        if (pg_elect()) {
+          pg_mma_ts<false>(tbase + kPgSCol, tbase, kd, idesc);
 #pragma unroll
-          for (int ks = 0; ks < kD / 16; ++ks) {
+          for (int ks = 1; ks < kD / 16; ++ks) {
             const uint32_t kb = ks >> 2, sub = ks & 3;
-            const uint64_t bd = desc_k_sw128(kvt + kb * kPgKVBlk + sub * 32);
-            if (kb < (uint32_t)kPgQTmemBlocks)
-              mma_f16_ts(tbase + kPgSCol, tbase + kb * 32 + sub * 8, bd, idesc, ks > 0 ? 1u : 0u);
-            else
-              mma_f16_ss(tbase + kPgSCol, desc_k_sw128(qa + (kb - kPgQTmemBlocks) * kPgQBlk + sub * 32), bd, idesc, 1u);
+            const uint32_t bd = kd + kb * (kPgKVBlk >> 4) + sub * 2;
+            if (kb < (uint32_t)kPgQTmemBlocks) pg_mma_ts<true>(tbase + kPgSCol, tbase + kb * 32 + sub * 8, bd, idesc);
+            else pg_mma_ss<true>(tbase + kPgSCol, qd + (kb - kPgQTmemBlocks) * (kPgQBlk >> 4) + sub * 2, bd, idesc);
           }
           mma_commit(s_full);
         }
-        if (ok) mma_commit(q_free);
-        ++seg;
+        __syncwarp();
       }
+    }
+    if (pg_elect()) {
       mma_commit(drain);
       mbar_wait(drain, 0u, &g_pg_error, kErrWaitAccFull);
     }
+    __syncwarp();
   } else if (warp == kPgWarpPV) {
     // ----------------------------------------------------------- PV issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_make_amn(kFmtF16, kFmtF16, 128, kPgRows);
-      const uint32_t kva = smem_u32(S.kv), pa = smem_u32(S.p);
-      PgWalk w;
-      uint32_t t = 0;
-      bool ok = true;
-      for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
-        const int nt = w.tiles();
-        for (int i = 0; i < nt; ++i, ++t) {
-          const uint32_t bi = t & 1u;
-          ok = mbar_wait(p_full + bi, (t >> 1) & 1u, &g_pg_error, kErrWaitAccFull);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t kvt = kva + bi * kPgKVBytes, pb = pa + bi * kPgPBytes;
+    constexpr uint32_t idesc = idesc_make_amn(kFmtF16, kFmtF16, 128, kPgRows);
+    const uint32_t kvd = pg_desc_mn(smem_u32(S.kv), kPgKVBlk), pd = pg_desc_k(smem_u32(S.p));
+    PgWalk w;
+    uint32_t t = 0;
+    bool ok = true;
+    for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
+      const int nt = w.tiles();
+      for (int i = 0; i < nt; ++i, ++t) {
+        const uint32_t bi = t & 1u;
+        ok = pg_wait_warp(p_full + bi, (t >> 1) & 1u, kErrWaitAccFull);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t vd = kvd + bi * (kPgKVBytes >> 4), pb = pd + bi * (kPgPBytes >> 4);
+        if (pg_elect()) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
 #pragma unroll
-            for (int ks = 0; ks < kPgE / 16; ++ks)
-              mma_f16_ss(tbase + kPgOCol + 64u * c,
-                         desc_mn_sw128(kvt + (uint32_t)(2 * c) * kPgKVBlk + (uint32_t)ks * 2048, kPgKVBlk, 1024),
-                         desc_k_sw128(pb + (uint32_t)ks * 32), idesc, (i > 0 || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < kPgE / 16; ++ks) {
+              const uint32_t ad = vd + 2 * c * (kPgKVBlk >> 4) + ks * (2048 >> 4), bd = pb + ks * 2;
+              if (ks == 0 && i == 0) pg_mma_ss<false>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
+              else pg_mma_ss<true>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
+            }
           }
           mma_commit(kv_free + bi);
           mma_commit(o_done);
+          if (i == nt - 1) mma_commit(acc_done);
         }
-        if (nt > 0 && ok) mma_commit(acc_done);
+        __syncwarp();
       }
+    }
+    if (pg_elect()) {
       mma_commit(drain + 1);
       mbar_wait(drain + 1, 0u, &g_pg_error, kErrWaitAccFull);
     }
+    __syncwarp();
   } else if (warp >= 4) {
-    // ---------------------------------------- entry loads, decoding, Q staging
+    // ---------------------------------------------- entry loads and decoding
     const int wq = warp - 4;
     PgCursor cu;                       // the tile whose page table values are fetched next
     cu.begin(a, S.start);
-    // page id (-1: no entry) and entry number in the page, of entry
-    // 8 wq + (lane & 7) of the tile whose entries are loaded next
+    // page id and entry number in the page of entry 8 wq + (lane & 7) of the
+    // tile whose entries are loaded next
     int id = -1;
     uint32_t slot = 0;
     auto lookup = [&]() {
@@ -531,164 +630,111 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         }
       }
     };
-    auto entry_ptr = [&]() -> const uint8_t* {
-      return id >= 0 && id < a.kv.n_pages ? a.kv.pages + (int64_t)id * a.kv.page_stride + (int64_t)slot * a.kv.row_stride
-                                          : nullptr;
-    };
     constexpr int kN = FP4 ? 4 : 8;    // 16-byte words per lane and tile
     uint4 r[kN];
-    uint2 sc = make_uint2(0, 0), scn = make_uint2(0, 0);
-    uint32_t vb = 0, vbn = 0;          // valid entries of this warp's 8
+    uint2 sc;
+    uint32_t vb;                       // valid entries of this warp's 8
+    // address of lane l's entry 8 wq + (l & 7); where there is none, the
+    // cache's first entry: every load is issued, and the decoder writes zeros
+    auto entry_ptr = [&](uint32_t& v) -> unsigned long long {
+      const bool on = id >= 0 && id < a.kv.n_pages;
+      v = __ballot_sync(0xffffffffu, on) & 0xFFu;
+      return (unsigned long long)(a.kv.pages + (on ? (int64_t)id * a.kv.page_stride + (int64_t)slot * a.kv.row_stride : 0));
+    };
     // FP8: word k is bytes [16 lane, 16 lane + 16) of entry k; FP4: bytes
     // [16 (lane & 15), ..) of entry 2k + (lane >> 4)
-    auto load_word = [&](const uint8_t* ptr, int k) -> uint4 {
-      const int e = FP4 ? 2 * k + (lane >> 4) : k;
-      const uint8_t* q = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)ptr, e));
-      return q ? ld_nc_v4(q + 16 * (FP4 ? lane & 15 : lane)) : make_uint4(0, 0, 0, 0);
+    auto load_word = [&](unsigned long long ptr, int k) -> uint4 {
+      const unsigned long long q = __shfl_sync(0xffffffffu, ptr, FP4 ? 2 * k + (lane >> 4) : k);
+      return ld_nc_v4(reinterpret_cast<const uint8_t*>(q) + 16 * (FP4 ? lane & 15 : lane));
     };
     // scales: lane 4e + w holds word w of entry e's scale bytes
-    auto load_scales = [&](const uint8_t* ptr) -> uint2 {
-      const uint8_t* q = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, (unsigned long long)ptr, lane >> 2));
-      if (!q) return make_uint2(0, 0);
-      if (FP4) return *reinterpret_cast<const uint2*>(q + kScaleOff + 8 * (lane & 3));
-      return make_uint2(*reinterpret_cast<const uint32_t*>(q + kScaleOff + 4 * (lane & 3)), 0);
+    auto load_scales = [&](unsigned long long ptr) -> uint2 {
+      const uint8_t* q = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, ptr, lane >> 2)) + kScaleOff;
+      if (FP4) return *reinterpret_cast<const uint2*>(q + 8 * (lane & 3));
+      return make_uint2(*reinterpret_cast<const uint32_t*>(q + 4 * (lane & 3)), 0);
     };
-    // the tile being decoded
-    PgCursor dc = cu;
+    int64_t tiles = 0;                 // key tiles of this CTA
+    {
+      PgWalk w;
+      for (bool go = w.begin(a, S.start); go; go = w.next(a)) tiles += w.tiles();
+    }
     lookup();
     {
-      const uint8_t* ptr = entry_ptr();
-      vb = __ballot_sync(0xffffffffu, ptr != nullptr) & 0xFFu;
+      const unsigned long long ptr = entry_ptr(vb);
 #pragma unroll
       for (int k = 0; k < kN; ++k) r[k] = load_word(ptr, k);
       sc = load_scales(ptr);
     }
     cu.advance(a);
     lookup();
-    uint32_t t = 0, seg = 0;
-    for (; dc.live; ++t) {
-      if (dc.i == 0) {
-        // ------------------------------------------------- an item begins: Q
-        if (seg > 0 && !pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty)) break;
-        tc_fence_after();
-        const PgWalk& w = dc.w;
-        const int n_rows = w.s.n * a.H - w.j * kPgRows;    // rows left in the sequence from this item on
-        const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q);
-        auto q_row = [&](int rr) -> const __nv_bfloat16* {
-          const int ri = w.j * kPgRows + rr, tok = ri / a.H;
-          return qb + (int64_t)(w.s.row0 + tok) * a.q_row_stride + (int64_t)(ri - tok * a.H) * a.q_head_stride;
-        };
-        {
-          const int rr = (32 * (warp & 3) + lane) & 63;
-          const bool on = rr < n_rows;
-          const uint4* src = reinterpret_cast<const uint4*>(q_row(on ? rr : 0)) + 24 * (wq >> 2);
-#pragma unroll 1
-          for (int u = 0; u < 6; u += 2) {                 // 32 columns: 64 channels
-            uint4 v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = on ? src[4 * u + k] : make_uint4(0, 0, 0, 0);
-            uint32_t o[2][16];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float f[8];
-              uint32_t ow[4];
-              pg_bf16x8(v[k], f);
-              pg_q_words<FP4>(f, ow);
-#pragma unroll
-              for (int m = 0; m < 4; ++m) o[k >> 2][4 * (k & 3) + m] = ow[m];
-            }
-            const uint32_t ta = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + 96u * (wq >> 2) + 16u * u;
-            tmem_st16(ta, o[0]);
-            tmem_st16(ta + 16, o[1]);
-          }
-          tmem_wait_st();
-        }
-        {
-          const int st = 32 * wq + lane;                   // 256 threads
-          uint4 v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = (st >> 4) + 16 * k;
-            v[k] = rr < n_rows ? *reinterpret_cast<const uint4*>(q_row(rr) + 384 + 8 * (st & 15)) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = (st >> 4) + 16 * k, c16 = st & 15;
-            float f[8];
-            pg_bf16x8(v[k], f);
-            if (a.rope_cs && c16 >= 8 && rr < n_rows) {    // channels 448 + 8 (c16 - 8) ..
-              const int tok = w.s.row0 + (w.j * kPgRows + rr) / a.H;
-              const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * (c16 - 8));
-              const float4 ca = cs[0], cb = cs[1];
-              float2 g;
-              g = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = g.x; f[1] = g.y;
-              g = rope_fwd(f[2], f[3], ca.z, ca.w); f[2] = g.x; f[3] = g.y;
-              g = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = g.x; f[5] = g.y;
-              g = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = g.x; f[7] = g.y;
-            }
-            uint32_t ow[4];
-            pg_q_words<FP4>(f, ow);
-            const uint4 o = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-            uint8_t* blk = S.q + (c16 >> 3) * kPgQBlk;
-            *reinterpret_cast<uint4*>(blk + sw128_offset_h(rr, 8 * (c16 & 7))) = o;
-            *reinterpret_cast<uint4*>(blk + sw128_offset_h(rr + 64, 8 * (c16 & 7))) = o;
-          }
-        }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-        ++seg;
-      }
-      // ------------------------------------------------------- decode the tile
+    for (uint32_t t = 0; (int64_t)t < tiles; ++t) {
       const uint32_t bi = t & 1u;
-      const uint8_t* nptr = entry_ptr();                   // entries of the next tile (nullptr: none)
-      vbn = __ballot_sync(0xffffffffu, nptr != nullptr) & 0xFFu;
-      cu.advance(a);
-      lookup();                                            // table values of the one after
-      scn = load_scales(nptr);
       if (t >= 2 && !pg_wait_warp(kv_free + bi, ((t >> 1) - 1) & 1u, kErrWaitSmemEmpty)) break;
       uint8_t* kt = S.kv + bi * kPgKVBytes;
+      if (FP4) {
+        const int l16 = lane & 15, kb = l16 >> 1;
+        uint8_t* blk = kt + kb * kPgKVBlk;
 #pragma unroll
-      for (int k = 0; k < kN; ++k) {
-        if (FP4) {
-          const int e = 2 * k + (lane >> 4), l16 = lane & 15;
+        for (int k = 0; k < kN; ++k) {
+          const int e = 2 * k + (lane >> 4);
           const uint32_t sx = __shfl_sync(0xffffffffu, sc.x, 4 * e + (l16 >> 2));
           const uint32_t sy = __shfl_sync(0xffffffffu, sc.y, 4 * e + (l16 >> 2));
-          const uint32_t two = ((l16 & 2) ? sy : sx) >> (16 * (l16 & 1));
+          uint32_t two = ((l16 & 2) ? sy : sx) >> (16 * (l16 & 1));
+          if (!((vb >> e) & 1u)) two = 0;                  // no entry: zeros
           const __half2 sa = pg_fp4_scale(two & 0xFF), sb = pg_fp4_scale((two >> 8) & 0xFF);
-          uint4 c[4] = {pg_decode_fp4(r[k].x, sa), pg_decode_fp4(r[k].y, sa), pg_decode_fp4(r[k].z, sb),
-                        pg_decode_fp4(r[k].w, sb)};
-          const int kb = l16 >> 1;
-          uint8_t* blk = kt + kb * kPgKVBlk;
-          const int row = 8 * wq + e;
+          const uint4 c[4] = {pg_decode_fp4(r[k].x, sa), pg_decode_fp4(r[k].y, sa), pg_decode_fp4(r[k].z, sb),
+                              pg_decode_fp4(r[k].w, sb)};
           // the four chunks in an order by block, so that 8 lanes' stores
           // meet 8 different 16-byte columns
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int cc = m ^ (kb & 3);
             const uint4 v = cc == 0 ? c[0] : cc == 1 ? c[1] : cc == 2 ? c[2] : c[3];
-            *reinterpret_cast<uint4*>(blk + sw128_offset_h(row, 32 * (l16 & 1) + 8 * cc)) = v;
+            *reinterpret_cast<uint4*>(blk + sw128_offset_h(8 * wq + e, 32 * (l16 & 1) + 8 * cc)) = v;
+          }
+        }
+      } else {
+        const int kb = lane >> 2, f = kb & 1;
+        uint8_t* blk = kt + kb * kPgKVBlk;
+        const bool on = (vb >> (lane >> 2)) & 1u;          // of the entry whose scales this lane holds
+        // any block of the warp's entries with a scale that fp16 cannot hold?
+        const bool far = on && __vcmpgtu4(__vsub4(sc.x, 0x69696969u), 0x1D1D1D1Du) != 0;
+        const uint32_t ex4 = on ? sc.x - 0x68686868u : 0u; // exponent fields of the fp16 factors; 0: factor 0
+        if (!__any_sync(0xffffffffu, far)) {
+#pragma unroll
+          for (int k = 0; k < kN; ++k) {
+            const uint32_t fe = (__shfl_sync(0xffffffffu, ex4, 4 * k + (lane >> 3)) >> (8 * ((lane >> 1) & 3))) & 0xFFu;
+            // odd blocks write their second chunk first, so that 8 lanes'
+            // stores meet 8 different 16-byte columns
+            uint4 c0, c1;
+            pg_decode_fp8(f ? make_uint4(r[k].z, r[k].w, r[k].x, r[k].y) : r[k], fe * 0x04000400u, c0, c1);
+            *reinterpret_cast<uint4*>(blk + sw128_offset_h(8 * wq + k, 16 * (lane & 3) + 8 * f)) = c0;
+            *reinterpret_cast<uint4*>(blk + sw128_offset_h(8 * wq + k, 16 * (lane & 3) + 8 * (f ^ 1))) = c1;
           }
         } else {
-          const uint32_t sx = __shfl_sync(0xffffffffu, sc.x, 4 * k + (lane >> 3));
-          const int ex = (int)((sx >> (8 * ((lane >> 1) & 3))) & 0xFF);
-          uint4 c0, c1;
-          pg_decode_fp8(r[k], ex, c0, c1);
-          const int kb = lane >> 2, row = 8 * wq + k, f = kb & 1;
-          uint8_t* blk = kt + kb * kPgKVBlk;
-          *reinterpret_cast<uint4*>(blk + sw128_offset_h(row, 16 * (lane & 3) + 8 * f)) = f ? c1 : c0;
-          *reinterpret_cast<uint4*>(blk + sw128_offset_h(row, 16 * (lane & 3) + 8 * (f ^ 1))) = f ? c0 : c1;
+#pragma unroll
+          for (int k = 0; k < kN; ++k) {
+            const uint32_t ex = (__shfl_sync(0xffffffffu, sc.x, 4 * k + (lane >> 3)) >> (8 * ((lane >> 1) & 3))) & 0xFFu;
+            uint4 c0 = make_uint4(0, 0, 0, 0), c1 = c0;
+            if ((vb >> k) & 1u) pg_decode_fp8_far(r[k], (int)ex, c0, c1);
+            *reinterpret_cast<uint4*>(blk + sw128_offset_h(8 * wq + k, 16 * (lane & 3))) = c0;
+            *reinterpret_cast<uint4*>(blk + sw128_offset_h(8 * wq + k, 16 * (lane & 3) + 8)) = c1;
+          }
         }
-        r[k] = load_word(nptr, k);
       }
       if (lane == 0) reinterpret_cast<uint8_t*>(S.valid)[8 * bi + wq] = (uint8_t)vb;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(kv_full + bi);
-      sc = scn;
-      vb = vbn;
-      dc.advance(a);
+      // the next tile's entries, all loads together (issued one by one between
+      // the decodes, each decode waits for the load before it: loads share
+      // their scoreboards), then the table values of the tile after it
+      const unsigned long long ptr = entry_ptr(vb);
+#pragma unroll
+      for (int k = 0; k < kN; ++k) r[k] = load_word(ptr, k);
+      sc = load_scales(ptr);
+      cu.advance(a);
+      lookup();
     }
   } else {
     // ------------------------------------------------------ softmax, output
@@ -701,7 +747,14 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     bool ok = true;
     int64_t meta_row0 = 0;
     int meta_rows = 0, meta_cont = 0, meta_done = 0;
-    for (bool go = w.begin(a, S.start); go; go = w.next(a)) {
+    bool go = w.begin(a, S.start);
+    // Q of an item is staged as soon as the one before has its last S read
+    auto stage = [&](const PgWalk& x) {
+      pg_stage_q<FP4>(a, x, S, trow, warp, lane);
+      if (lane == 0) mbar_arrive(q_full);
+    };
+    if (go && w.tiles() > 0) stage(w);
+    while (go) {
       const int nt = w.tiles();
       const int n_rows = w.s.n * a.H - w.j * kPgRows;
       const int ri = w.j * kPgRows + rr;
@@ -791,6 +844,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + bi);
       }
+      PgWalk nx = w;
+      go = nx.next(a);
+      if (go && nx.tiles() > 0) stage(nx);
       // ------------------------------------------------------------ output
       const bool whole = w.take == w.units;
       S.lx[64 * part + rr] = l_run;
@@ -823,44 +879,46 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       if (nt > 0) ok = ok && pg_wait_warp(acc_done, seg++ & 1u, kErrWaitAccFull);
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int ch = 0; ch < 8; ++ch) {               // 128 channels x 32 rows at a time
+        const int c = ch >> 1, k0 = 32 * (ch & 1);
         const int d = pg_channel<FP4>(128 * c + 32 * warp + lane);
-        uint32_t o[64];
+        if (k0 >= n_rows) continue;
+        uint32_t o[32];
         if (nt > 0 && ok) {
-          tmem_ld64(trow + kPgOCol + 64 * c, o);
+          tmem_ld32(trow + kPgOCol + 64 * c + k0, o);
           tmem_wait_ld();
         } else {
 #pragma unroll
-          for (int k = 0; k < 64; ++k) o[k] = 0u;
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
         if (whole) {
           if (a.rope_cs && d >= kRopeStart) {          // whole warps: 32 channels from 448 or 480
 #pragma unroll
-            for (int k = 0; k < 64; ++k) {
+            for (int k = 0; k < 32; ++k) {
               const float v = __uint_as_float(o[k]);
               const float u = __shfl_xor_sync(0xffffffffu, v, 2);   // channel d ^ 1
-              const int tok = w.s.row0 + (w.j * kPgRows + min(k, n_rows - 1)) / a.H;
+              const int tok = w.s.row0 + (w.j * kPgRows + min(k0 + k, n_rows - 1)) / a.H;
               const float2 cs = *reinterpret_cast<const float2*>(a.rope_cs + (int64_t)tok * 64 + ((d - kRopeStart) & ~1));
               o[k] = __float_as_uint((d & 1) ? v * cs.x - u * cs.y : v * cs.x + u * cs.y);
             }
           }
           // rows k, k + 1: the lane of the even channel stores row k's pair of
           // channels, the lane of the odd one row k + 1's
-          __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + orow * kD + (d & ~1);
+          __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + (orow + k0) * kD + (d & ~1);
           const int odd = d & 1;
 #pragma unroll
-          for (int k = 0; k < 64; k += 2) {
-            const float v0 = __uint_as_float(o[k]) * S.scl[k], v1 = __uint_as_float(o[k + 1]) * S.scl[k + 1];
+          for (int k = 0; k < 32; k += 2) {
+            const float v0 = __uint_as_float(o[k]) * S.scl[k0 + k], v1 = __uint_as_float(o[k + 1]) * S.scl[k0 + k + 1];
             const float u = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 2);
-            if (k + odd < n_rows)
+            if (k0 + k + odd < n_rows)
               *reinterpret_cast<__nv_bfloat162*>(ob + (int64_t)(k + odd) * kD) =
                   odd ? __floats2bfloat162_rn(u, v1) : __floats2bfloat162_rn(v0, u);
           }
         } else {
-          float* po = p.part_o + (int64_t)slot * (64 * kD) + d;
+          float* po = p.part_o + (int64_t)slot * (64 * kD) + k0 * kD + d;
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (k < n_rows) po[k * kD] = __uint_as_float(o[k]);
+          for (int k = 0; k < 32; ++k)
+            if (k0 + k < n_rows) po[k * kD] = __uint_as_float(o[k]);
         }
       }
       tc_fence_before();
@@ -873,6 +931,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
           meta_row0 = orow;
         }
       }
+      w = nx;
     }
     if (tid == 0) p.meta[blockIdx.x] = PgMeta{meta_row0, meta_rows, meta_cont, meta_done, 0};
   }
