@@ -3,15 +3,15 @@
 // partial RoPE, FP8 or FP4 entries, one token per sequence up to whole prompts.
 //
 // A work item is 64 query rows (token, head) of one sequence, rows in (token,
-// head) order, so any head count fills the tile; it runs over the 64-entry
+// head) order, so any head count fills the tile; it runs over the 32-entry
 // key tiles its rows see.  Per key tile, with K = V = the decoded entries:
 //   S  = Q K^T    tcgen05.mma kind::f16, M = 128 TMEM lanes holding the 64
-//                 rows twice (lane L: row L mod 64), N = 64 entries, K = 512.
+//                 rows twice (lane L: row L mod 64), N = 32 entries, K = 512.
 //                 Channels 0..383 of Q are the A operand in TMEM, the last
 //                 128 in shared memory.  The two copies let four softmax
-//                 warps share a tile: warps 0-1 take entries 0..31 of rows
-//                 0..63, warps 2-3 entries 32..63.
-//   O^T += V^T P^T  M = 128 latent channels (4 chunks), N = 64 rows, K = 64
+//                 warps share a tile: warps 0-1 take entries 0..15 of rows
+//                 0..63, warps 2-3 entries 16..31.
+//   O^T += V^T P^T  M = 128 latent channels (4 chunks), N = 64 rows, K = 32
 //                 entries: 4 x 64 TMEM columns, where O (64 x 512) would take
 //                 all 512.  The shared-memory tile of decoded entries is the
 //                 K-major B operand of S and the MN-major A operand here.
@@ -20,16 +20,17 @@
 // held in fp16 times 2^6: at most 2^14, and weights down to 2^-31 of the max
 // keep a value.
 //
-// Work split: every key tile of every item is one unit (an item that sees no
-// entry is one unit too); CTA i takes units [iU/G, (i+1)U/G) of the batch in
-// order, whatever the sequences' lengths, and computes where that is from the
-// lengths on the device.  An item that ends up in several CTAs leaves
-// (max, sum, O^T) partials in the workspace, at most two per CTA, which
-// paged_attn_combine joins in CTA order; the result does not depend on timing.
+// Work split: the batch is a line on which an item of T key tiles takes
+// kPgItemCost + T; CTA i takes the tiles on [iU/G, (i+1)U/G) of its length U,
+// whatever the sequences' lengths, and computes where that is from the lengths
+// on the device.  An item that ends up in several CTAs leaves (max, sum, O^T)
+// partials in the workspace, at most two per CTA, which paged_attn_combine
+// joins in CTA order; the result does not depend on timing.
 //
-// Warp roles: 0-3 staging of Q, softmax and output, 4-11 entry loads and
-// decoding, 12 issues the S MMAs, 13 the PV MMAs.  Entry tiles and P are double buffered; the entries of tile t + 1 are loaded
-// into registers as tile t's are decoded, page table values one tile earlier.
+// Warp roles: 0-3 softmax and output, 4-7 and 8-11 staging of Q and loading and
+// decoding of even and odd tiles, 12 issues the S MMAs, 13 the PV MMAs.  Four
+// entry tiles and P tiles are in flight: a tile's way (decode, S, softmax, PV)
+// is several times longer than its share of the tensor pipe.
 #include <climits>
 
 #include "sm100.cuh"
@@ -39,8 +40,9 @@
 namespace csa {
 
 constexpr int kPgRows = 64;               // query rows per item
-constexpr int kPgE = 64;                  // entries per key tile
-constexpr int kPgDeqWarps = 8;
+constexpr int kPgE = 32;                  // entries per key tile
+constexpr int kPgBufs = 4;                // entry tiles (and P tiles) in the ring
+constexpr int kPgDeqWarps = 8;            // two groups of 4: even and odd tiles
 constexpr int kPgWarpS = 4 + kPgDeqWarps;
 constexpr int kPgWarpPV = kPgWarpS + 1;
 constexpr int kPgWarps = kPgWarpPV + 1;
@@ -50,16 +52,18 @@ constexpr int kPgQBlk = 128 * 128;        // shared Q block: 128 rows x 64 fp16
 constexpr int kPgKVBlk = kPgE * 128;      // 64-channel block of an entry tile
 constexpr int kPgKVBytes = 8 * kPgKVBlk;
 constexpr int kPgPBytes = kPgRows * kPgE * 2;
-constexpr uint32_t kPgSCol = 32 * kPgQTmemBlocks;
+constexpr uint32_t kPgSCol = 32 * kPgQTmemBlocks;   // two S tiles of 32 columns
 constexpr uint32_t kPgOCol = 256;
 constexpr uint32_t kPgTmemCols = 512;
+static_assert(kPgSCol + 2 * kPgE <= kPgOCol, "TMEM map");
+constexpr int kPgItemCost = 4;            // an item's own cost (Q, output) in key tiles
 constexpr float kPgRescale = 8.0f;        // lazy-rescale threshold (exp2 units)
 constexpr float kPgPExp = 6.0f;           // P carries a factor 2^6
 constexpr float kPgLog2e = 1.4426950408889634f;
 constexpr float kPgLn2 = 0.6931471805599453f;
 constexpr int kPgMaxB = 65536;
-constexpr size_t kPgSmemBytes = 1024 + 2 * kPgQBlk + 2 * kPgKVBytes + 2 * kPgPBytes + 4096;
-static_assert(kPgMaxB / 32 * 8 <= 2 * kPgKVBytes, "the plan's group sums use the entry tiles");
+constexpr size_t kPgSmemBytes = 1024 + 2 * kPgQBlk + kPgBufs * (kPgKVBytes + kPgPBytes) + 4096;
+static_assert(kPgMaxB / 32 * 8 <= kPgBufs * kPgKVBytes, "the plan's group sums use the entry tiles");
 
 static __device__ int g_pg_error;
 
@@ -83,14 +87,14 @@ struct PgParams {
 
 struct PgSmem {
   uint8_t* q;        // channels 384..511 of Q: 2 blocks of 128 rows
-  uint8_t* kv;       // 2 entry tiles
-  uint8_t* p;        // 2 x P
+  uint8_t* kv;       // [kPgBufs] entry tiles
+  uint8_t* p;        // [kPgBufs] P tiles
   float* mx;         // [2][2][64] tile maxima by tile parity and entry half
   float* alpha;      // [64] rescale factors
   float* lx;         // [2][64] sums of the entry halves
   float* scl;        // [64] output factors
-  uint32_t* valid;   // [2][2] entries present, by tile parity
-  int64_t* start;    // this CTA's range: {first unit's offset in its item, units, sequence, tile}
+  uint32_t* valid;   // [kPgBufs] entries present in a tile
+  int64_t* start;    // this CTA's range: {its start inside its first item, length, sequence, item}
   uint64_t* bars;
   uint32_t* tmem_base;
 };
@@ -99,13 +103,13 @@ CSA_DEV PgSmem carve_pg(uint8_t* raw) {
   PgSmem s;
   uint8_t* p = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   s.q = p; p += 2 * kPgQBlk;
-  s.kv = p; p += 2 * kPgKVBytes;
-  s.p = p; p += 2 * kPgPBytes;
+  s.kv = p; p += kPgBufs * kPgKVBytes;
+  s.p = p; p += kPgBufs * kPgPBytes;
   s.mx = reinterpret_cast<float*>(p); p += 4 * 64 * 4;
   s.alpha = reinterpret_cast<float*>(p); p += 64 * 4;
   s.lx = reinterpret_cast<float*>(p); p += 2 * 64 * 4;
   s.scl = reinterpret_cast<float*>(p); p += 64 * 4;
-  s.bars = reinterpret_cast<uint64_t*>(p); p += 16 * 8;
+  s.bars = reinterpret_cast<uint64_t*>(p); p += 24 * 8;
   s.start = reinterpret_cast<int64_t*>(p); p += 4 * 8;
   s.valid = reinterpret_cast<uint32_t*>(p); p += 4 * 4;
   s.tmem_base = reinterpret_cast<uint32_t*>(p);
@@ -144,6 +148,15 @@ CSA_DEV void pg_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t ides
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}"
       ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDescK), "n"(ACC ? 1 : 0) : "memory");
 }
+// P rows are 64 bytes (32 fp16): 64-byte swizzle for that operand.
+constexpr uint32_t kPgDescP = (512u >> 4) | 1u << 14 | 4u << 29;
+template <bool ACC>
+CSA_DEV void pg_mma_pv(uint32_t d, uint32_t v_lo, uint32_t p_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
+      ::"r"(d), "r"(v_lo), "r"(p_lo), "r"(idesc), "n"(kPgDescK), "n"(kPgDescP), "n"(ACC ? 1 : 0) : "memory");
+}
 CSA_DEV bool pg_elect() {
   uint32_t e;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
@@ -175,43 +188,57 @@ CSA_DEV void pg_item(const csa_paged_attn_args& a, const PgSeq& s, int j, int& k
   k0 = a.window ? max(0, p0 + 1 > a.window ? p0 + 1 - a.window : 0) : 0;
   if (k1 < k0) k1 = k0;
 }
-CSA_DEV int pg_units(int k0, int k1) { return max(1, (k1 - k0 + kPgE - 1) / kPgE); }
+CSA_DEV int pg_tiles(int k0, int k1) { return (k1 - k0 + kPgE - 1) / kPgE; }
 
-// The CTA's walk over its items.
+// The CTA's walk over its items.  An item of T key tiles spans kPgItemCost + T
+// of the cost axis; the CTA takes the tiles whose place lies in its range.
 struct PgWalk {
-  int64_t left;    // units left, this item's included
-  int b, j, off;   // sequence, item, first key tile of the item taken here
+  int64_t left;    // cost left, from this item's start in the range on
+  int b, j;        // sequence, item
+  int at;          // where in the item the range starts
   PgSeq s;
-  int k0, k1, units, take;   // take: units of this item taken here
+  int k0, k1, total;   // the item's positions and key tiles
+  int off, take;       // first key tile taken here, number taken
   CSA_DEV void item(const csa_paged_attn_args& a) {
     pg_item(a, s, j, k0, k1);
-    units = pg_units(k0, k1);
-    take = (int)min((int64_t)(units - off), left);
+    total = pg_tiles(k0, k1);
+    off = min(max(at - kPgItemCost, 0), total);
+    take = (int)min((int64_t)total, max(at + left - kPgItemCost, (int64_t)0)) - off;
+  }
+  // does this CTA do anything for the item? (a tileless one belongs to the
+  // CTA at its start)
+  CSA_DEV bool mine() const { return take > 0 || (total == 0 && at == 0); }
+  CSA_DEV void settle(const csa_paged_attn_args& a) {
+    while (left > 0 && !mine()) step(a);
+  }
+  CSA_DEV void step(const csa_paged_attn_args& a) {
+    left -= kPgItemCost + total - at;
+    at = 0;
+    if (left <= 0) return;
+    if (++j >= s.tiles) {
+      j = 0;
+      do {
+        if (++b >= a.kv.B) { left = 0; return; }
+        s = pg_seq(a, b);
+      } while (s.tiles == 0);
+    }
+    item(a);
   }
   CSA_DEV bool begin(const csa_paged_attn_args& a, const int64_t* start) {
-    off = (int)start[0];
+    at = (int)start[0];
     left = start[1];
     b = (int)start[2];
     j = (int)start[3];
     if (left <= 0) return false;
     s = pg_seq(a, b);
     item(a);
-    return true;
+    settle(a);
+    return left > 0;
   }
-  CSA_DEV int tiles() const { return k1 > k0 ? take : 0; }
   CSA_DEV bool next(const csa_paged_attn_args& a) {
-    left -= take;
-    if (left <= 0) return false;
-    off = 0;
-    if (++j >= s.tiles) {
-      j = 0;
-      do {
-        if (++b >= a.kv.B) { left = 0; return false; }
-        s = pg_seq(a, b);
-      } while (s.tiles == 0);
-    }
-    item(a);
-    return true;
+    step(a);
+    settle(a);
+    return left > 0;
   }
 };
 
@@ -220,9 +247,9 @@ CSA_DEV int64_t pg_warp_sum64(int64_t v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// Units of sequences 32 g + lane (0 past the last).  Sequences with many
+// Cost of sequences 32 g + lane (0 past the last).  Sequences with many
 // items are summed by the whole warp.
-CSA_DEV int64_t pg_group_units(const csa_paged_attn_args& a, int g, int lane) {
+CSA_DEV int64_t pg_group_cost(const csa_paged_attn_args& a, int g, int lane) {
   const int b = 32 * g + lane;
   PgSeq s{0, 0, 0, 0};
   if (b < a.kv.B) s = pg_seq(a, b);
@@ -231,7 +258,7 @@ CSA_DEV int64_t pg_group_units(const csa_paged_attn_args& a, int g, int lane) {
     for (int j = 0; j < s.tiles; ++j) {
       int k0, k1;
       pg_item(a, s, j, k0, k1);
-      u += pg_units(k0, k1);
+      u += kPgItemCost + pg_tiles(k0, k1);
     }
   }
   for (uint32_t big = __ballot_sync(0xffffffffu, s.tiles > 4); big; big &= big - 1) {
@@ -245,7 +272,7 @@ CSA_DEV int64_t pg_group_units(const csa_paged_attn_args& a, int g, int lane) {
     for (int j = lane; j < q.tiles; j += 32) {
       int k0, k1;
       pg_item(a, q, j, k0, k1);
-      v += pg_units(k0, k1);
+      v += kPgItemCost + pg_tiles(k0, k1);
     }
     v = pg_warp_sum64(v);
     if (lane == l) u = v;
@@ -266,12 +293,12 @@ CSA_DEV int pg_locate(int64_t v, int64_t& at, int lane) {
   at -= before;
   return l < 0 ? 0 : l;
 }
-// Finds the CTA's range of units; every warp of the CTA takes part.
+// Finds the CTA's range of the cost axis; every warp of the CTA takes part.
 CSA_DEV void pg_plan(const csa_paged_attn_args& a, const PgSmem& S, int warp, int lane) {
   int64_t* gsum = reinterpret_cast<int64_t*>(S.kv);
   const int groups = (a.kv.B + 31) / 32;
   for (int g = warp; g < groups; g += kPgWarps) {
-    const int64_t u = pg_warp_sum64(pg_group_units(a, g, lane));
+    const int64_t u = pg_warp_sum64(pg_group_cost(a, g, lane));
     if (lane == 0) gsum[g] = u;
   }
   __syncthreads();
@@ -279,7 +306,7 @@ CSA_DEV void pg_plan(const csa_paged_attn_args& a, const PgSmem& S, int warp, in
     int64_t total = 0;
     for (int g = lane; g < groups; g += 32) total += gsum[g];
     total = pg_warp_sum64(total);
-    const int64_t G = min((int64_t)gridDim.x, total);
+    const int64_t G = min((int64_t)gridDim.x, (total + 1) / 2);
     int64_t u0 = 0, u1 = 0;
     if ((int64_t)blockIdx.x < G) {
       u0 = total * blockIdx.x / G;
@@ -298,7 +325,7 @@ CSA_DEV void pg_plan(const csa_paged_attn_args& a, const PgSmem& S, int warp, in
         }
         at -= sum;
       }
-      const int64_t v = pg_group_units(a, base, lane);     // the sequence
+      const int64_t v = pg_group_cost(a, base, lane);     // the sequence
       b = 32 * base + pg_locate(v, at, lane);
       const PgSeq s = pg_seq(a, b);
       for (;; j += 32) {                                   // the item
@@ -306,7 +333,7 @@ CSA_DEV void pg_plan(const csa_paged_attn_args& a, const PgSmem& S, int warp, in
         if (j + lane < s.tiles) {
           int k0, k1;
           pg_item(a, s, j + lane, k0, k1);
-          w = pg_units(k0, k1);
+          w = kPgItemCost + pg_tiles(k0, k1);
         }
         const int64_t sum = pg_warp_sum64(w);
         if (at < sum || j + 32 >= s.tiles) {
@@ -403,76 +430,83 @@ CSA_DEV __half2 pg_fp4_scale(uint32_t code) {   // E4M3 scale * 2^7, twice
   return __hmul2(pg_u2h(pg_e4m3_02(code | (code << 16))), pg_u2h(0x78007800u));
 }
 
-// Stages an item's 64 query rows: channels 0..383 into TMEM lanes 32 warp ..
-// (twice: lanes L and L + 64 hold row L), channels 384..511 into the two
-// shared blocks.  Called by warps 0-3; rows past the sequence are zero.
-template <bool FP4>
-CSA_DEV void pg_stage_q(const csa_paged_attn_args& a, const PgWalk& w, const PgSmem& S, uint32_t trow, int warp, int lane) {
+// Stages half g of an item's 64 query rows: channels 192 g .. 192 g + 191 into
+// TMEM (twice: lanes L and L + 64 hold row L), channels 384 + 64 g .. into
+// shared block g.  Called by the 4 warps of decode group g; rows past the
+// sequence are zero.  Loads are issued before the wait for the operand's last
+// reader.
+template <bool FP4, typename Wait>
+CSA_DEV bool pg_stage_q(const csa_paged_attn_args& a, const PgWalk& w, uint8_t* qblk, uint32_t tbase, int warp, int lane, int g,
+                        Wait wait) {
   const int n_rows = w.s.n * a.H - w.j * kPgRows;          // rows left in the sequence from this item on
   const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q);
   auto q_row = [&](int rr) -> const __nv_bfloat16* {
     const int ri = w.j * kPgRows + rr, tok = ri / a.H;
     return qb + (int64_t)(w.s.row0 + tok) * a.q_row_stride + (int64_t)(ri - tok * a.H) * a.q_head_stride;
   };
-  {
-    const int rr = 32 * (warp & 1) + lane;
-    const bool on = rr < n_rows;
-    const uint4* src = reinterpret_cast<const uint4*>(q_row(on ? rr : 0));
+  const int wl = warp & 3, rr = (32 * wl + lane) & 63;
+  const bool on = rr < n_rows;
+  const uint4* src = reinterpret_cast<const uint4*>(q_row(on ? rr : 0)) + 24 * g;
+  bool ok = true;
 #pragma unroll 1
-    for (int u = 0; u < 12; u += 2) {                      // 32 columns: 64 channels
-      uint4 v[8];
+  for (int u = 0; u < 2; ++u) {                            // 48 columns: 96 channels
+    uint4 v[12];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = on ? src[4 * u + k] : make_uint4(0, 0, 0, 0);
-      uint32_t o[2][16];
+    for (int k = 0; k < 12; ++k) v[k] = on ? src[12 * u + k] : make_uint4(0, 0, 0, 0);
+    if (u == 0) {
+      ok = wait();
+      if (!ok) break;
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+    for (int q = 0; q < 3; ++q) {
+      uint32_t o[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
         float f[8];
         uint32_t ow[4];
-        pg_bf16x8(v[k], f);
+        pg_bf16x8(v[4 * q + k], f);
         pg_q_words<FP4>(f, ow);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) o[k >> 2][4 * (k & 3) + m] = ow[m];
+        for (int m = 0; m < 4; ++m) o[4 * k + m] = ow[m];
       }
-      tmem_st16(trow + 16u * u, o[0]);
-      tmem_st16(trow + 16u * u + 16, o[1]);
+      tmem_st16(tbase + ((uint32_t)(32 * wl) << 16) + 96u * g + 48u * u + 16u * q, o);
     }
   }
-  const int st = 32 * warp + lane;                         // 128 threads
-#pragma unroll 1
-  for (int k0 = 0; k0 < 8; k0 += 4) {
+  if (ok) {
+    const int st = 32 * wl + lane, c8 = st & 7;            // 128 threads: 16 rows x 8 chunks, 4 times
     uint4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int rr = (st >> 4) + 8 * (k0 + k);
-      v[k] = rr < n_rows ? *reinterpret_cast<const uint4*>(q_row(rr) + 384 + 8 * (st & 15)) : make_uint4(0, 0, 0, 0);
+      const int r = (st >> 3) + 16 * k;
+      v[k] = r < n_rows ? *reinterpret_cast<const uint4*>(q_row(r) + 384 + 64 * g + 8 * c8) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int rr = (st >> 4) + 8 * (k0 + k), c16 = st & 15;
+      const int r = (st >> 3) + 16 * k;
       float f[8];
       pg_bf16x8(v[k], f);
-      if (a.rope_cs && c16 >= 8 && rr < n_rows) {          // channels 448 + 8 (c16 - 8) ..
-        const int tok = w.s.row0 + (w.j * kPgRows + rr) / a.H;
-        const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * (c16 - 8));
+      if (a.rope_cs && g == 1 && r < n_rows) {             // channels 448 + 8 c8 ..
+        const int tok = w.s.row0 + (w.j * kPgRows + r) / a.H;
+        const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * c8);
         const float4 ca = cs[0], cb = cs[1];
-        float2 g;
-        g = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = g.x; f[1] = g.y;
-        g = rope_fwd(f[2], f[3], ca.z, ca.w); f[2] = g.x; f[3] = g.y;
-        g = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = g.x; f[5] = g.y;
-        g = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = g.x; f[7] = g.y;
+        float2 x;
+        x = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = x.x; f[1] = x.y;
+        x = rope_fwd(f[2], f[3], ca.z, ca.w); f[2] = x.x; f[3] = x.y;
+        x = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = x.x; f[5] = x.y;
+        x = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = x.x; f[7] = x.y;
       }
       uint32_t ow[4];
       pg_q_words<FP4>(f, ow);
       const uint4 o = make_uint4(ow[0], ow[1], ow[2], ow[3]);
-      uint8_t* blk = S.q + (c16 >> 3) * kPgQBlk;
-      *reinterpret_cast<uint4*>(blk + sw128_offset_h(rr, 8 * (c16 & 7))) = o;
-      *reinterpret_cast<uint4*>(blk + sw128_offset_h(rr + 64, 8 * (c16 & 7))) = o;
+      *reinterpret_cast<uint4*>(qblk + sw128_offset_h(r, 8 * c8)) = o;
+      *reinterpret_cast<uint4*>(qblk + sw128_offset_h(r + 64, 8 * c8)) = o;
     }
+    tmem_wait_st();
+    fence_proxy_async_smem();
+    tc_fence_before();
   }
-  tmem_wait_st();
-  fence_proxy_async_smem();
-  tc_fence_before();
   __syncwarp();
+  return ok;
 }
 
 // A position in the CTA's list of key tiles.
@@ -480,20 +514,17 @@ struct PgCursor {
   PgWalk w;
   int i;           // tile of the item
   bool live;
-  CSA_DEV void settle(const csa_paged_attn_args& a) {   // skip items that see no entry
-    while (live && w.tiles() == 0) live = w.next(a);
-  }
-  CSA_DEV void begin(const csa_paged_attn_args& a, const int64_t* start) {
+  CSA_DEV void begin(const csa_paged_attn_args& a, const int64_t* start, int skip) {
     live = w.begin(a, start);
     i = 0;
-    settle(a);
+    advance(a, skip);
   }
-  CSA_DEV void advance(const csa_paged_attn_args& a) {
-    if (!live) return;
-    if (++i < w.tiles()) return;
-    i = 0;
-    live = w.next(a);
-    settle(a);
+  CSA_DEV void advance(const csa_paged_attn_args& a, int n) {
+    i += n;
+    while (live && i >= w.take) {
+      i -= w.take;
+      live = w.next(a);
+    }
   }
 };
 
@@ -503,28 +534,30 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   const PgSmem S = carve_pg(smem_raw);
-  uint64_t* kv_full = S.bars + 0;    // [2] tile decoded (8 warp arrivals)
-  uint64_t* kv_free = S.bars + 2;    // [2] PV done: entry tile and P reusable
-  uint64_t* s_full = S.bars + 4;     // S in TMEM
-  uint64_t* s_free = S.bars + 5;     // S read by the softmax (4 warp arrivals)
-  uint64_t* p_full = S.bars + 6;     // [2] P written, O^T rescaled (4 warp arrivals)
-  uint64_t* o_done = S.bars + 8;     // one phase per PV
-  uint64_t* q_full = S.bars + 9;     // an item's Q staged (4 warp arrivals)
-  uint64_t* acc_done = S.bars + 11;  // an item's last PV done (one phase per item)
-  uint64_t* drain = S.bars + 12;     // [2] all MMAs of an issuer retired (teardown)
+  uint64_t* kv_full = S.bars + 0;    // [kPgBufs] tile decoded (4 warp arrivals)
+  uint64_t* kv_free = S.bars + 4;    // [kPgBufs] PV done: entry tile and P tile reusable
+  uint64_t* p_full = S.bars + 8;     // [kPgBufs] P written, O^T rescaled (4 warp arrivals)
+  uint64_t* s_full = S.bars + 12;    // [2] S in TMEM
+  uint64_t* s_free = S.bars + 14;    // [2] S read by the softmax (4 warp arrivals)
+  uint64_t* q_full = S.bars + 16;    // an item's Q staged (8 warp arrivals)
+  uint64_t* q_free = S.bars + 17;    // an item's last S done
+  uint64_t* acc_done = S.bars + 18;  // an item's last PV done
+  uint64_t* drain = S.bars + 19;     // [2] all MMAs of an issuer retired (teardown)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const csa_paged_attn_args& a = p.a;
   if (tid == 0) {
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(kv_full + k, kPgDeqWarps);
+    for (int k = 0; k < kPgBufs; ++k) {
+      mbar_init(kv_full + k, 4);
       mbar_init(kv_free + k, 1);
       mbar_init(p_full + k, 4);
+    }
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(s_full + k, 1);
+      mbar_init(s_free + k, 4);
       mbar_init(drain + k, 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 4);
-    mbar_init(o_done, 1);
-    mbar_init(q_full, 4);
+    mbar_init(q_full, kPgDeqWarps);
+    mbar_init(q_free, 1);
     mbar_init(acc_done, 1);
     fence_mbar_init();
   }
@@ -544,26 +577,26 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     uint32_t t = 0, seg = 0;
     bool ok = true;
     for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
-      const int nt = w.tiles();
-      if (nt == 0) continue;
+      if (w.take == 0) continue;
       ok = pg_wait_warp(q_full, seg++ & 1u, kErrWaitTmaFull);
-      for (int i = 0; i < nt && ok; ++i, ++t) {
-        const uint32_t bi = t & 1u;
-        ok = pg_wait_warp(kv_full + bi, (t >> 1) & 1u, kErrWaitTmaFull);
-        if (ok && t >= 1) ok = pg_wait_warp(s_free, (t - 1) & 1u, kErrWaitAccEmpty);
+      for (int i = 0; i < w.take && ok; ++i, ++t) {
+        const uint32_t bi = t % kPgBufs;
+        ok = pg_wait_warp(kv_full + bi, (t / kPgBufs) & 1u, kErrWaitTmaFull);
+        if (ok && t >= 2) ok = pg_wait_warp(s_free + (t & 1u), ((t >> 1) - 1) & 1u, kErrWaitAccEmpty);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t kd = kvd + bi * (kPgKVBytes >> 4);
+        const uint32_t kd = kvd + bi * (kPgKVBytes >> 4), sd = tbase + kPgSCol + kPgE * (t & 1u);
         if (pg_elect()) {
-          pg_mma_ts<false>(tbase + kPgSCol, tbase, kd, idesc);
+          pg_mma_ts<false>(sd, tbase, kd, idesc);
 #pragma unroll
           for (int ks = 1; ks < kD / 16; ++ks) {
             const uint32_t kb = ks >> 2, sub = ks & 3;
             const uint32_t bd = kd + kb * (kPgKVBlk >> 4) + sub * 2;
-            if (kb < (uint32_t)kPgQTmemBlocks) pg_mma_ts<true>(tbase + kPgSCol, tbase + kb * 32 + sub * 8, bd, idesc);
-            else pg_mma_ss<true>(tbase + kPgSCol, qd + (kb - kPgQTmemBlocks) * (kPgQBlk >> 4) + sub * 2, bd, idesc);
+            if (kb < (uint32_t)kPgQTmemBlocks) pg_mma_ts<true>(sd, tbase + kb * 32 + sub * 8, bd, idesc);
+            else pg_mma_ss<true>(sd, qd + (kb - kPgQTmemBlocks) * (kPgQBlk >> 4) + sub * 2, bd, idesc);
           }
-          mma_commit(s_full);
+          mma_commit(s_full + (t & 1u));
+          if (i == w.take - 1) mma_commit(q_free);
         }
         __syncwarp();
       }
@@ -581,10 +614,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     uint32_t t = 0;
     bool ok = true;
     for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
-      const int nt = w.tiles();
-      for (int i = 0; i < nt; ++i, ++t) {
-        const uint32_t bi = t & 1u;
-        ok = pg_wait_warp(p_full + bi, (t >> 1) & 1u, kErrWaitAccFull);
+      for (int i = 0; i < w.take; ++i, ++t) {
+        const uint32_t bi = t % kPgBufs;
+        ok = pg_wait_warp(p_full + bi, (t / kPgBufs) & 1u, kErrWaitAccFull);
         if (!ok) break;
         tc_fence_after();
         const uint32_t vd = kvd + bi * (kPgKVBytes >> 4), pb = pd + bi * (kPgPBytes >> 4);
@@ -594,13 +626,12 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
             for (int ks = 0; ks < kPgE / 16; ++ks) {
               const uint32_t ad = vd + 2 * c * (kPgKVBlk >> 4) + ks * (2048 >> 4), bd = pb + ks * 2;
-              if (ks == 0 && i == 0) pg_mma_ss<false>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
-              else pg_mma_ss<true>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
+              if (ks == 0 && i == 0) pg_mma_pv<false>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
+              else pg_mma_pv<true>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
             }
           }
           mma_commit(kv_free + bi);
-          mma_commit(o_done);
-          if (i == nt - 1) mma_commit(acc_done);
+          if (i == w.take - 1) mma_commit(acc_done);
         }
         __syncwarp();
       }
@@ -612,9 +643,10 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     __syncwarp();
   } else if (warp >= 4) {
     // ---------------------------------------------- entry loads and decoding
-    const int wq = warp - 4;
+    // Group g (4 warps) takes the CTA's tiles of parity g, 8 entries a warp.
+    const int wq = (warp - 4) & 3, g = (warp - 4) >> 2;
     PgCursor cu;                       // the tile whose page table values are fetched next
-    cu.begin(a, S.start);
+    cu.begin(a, S.start, g);
     // page id and entry number in the page of entry 8 wq + (lane & 7) of the
     // tile whose entries are loaded next
     int id = -1;
@@ -653,11 +685,6 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       if (FP4) return *reinterpret_cast<const uint2*>(q + 8 * (lane & 3));
       return make_uint2(*reinterpret_cast<const uint32_t*>(q + 4 * (lane & 3)), 0);
     };
-    int64_t tiles = 0;                 // key tiles of this CTA
-    {
-      PgWalk w;
-      for (bool go = w.begin(a, S.start); go; go = w.next(a)) tiles += w.tiles();
-    }
     lookup();
     {
       const unsigned long long ptr = entry_ptr(vb);
@@ -665,11 +692,29 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       for (int k = 0; k < kN; ++k) r[k] = load_word(ptr, k);
       sc = load_scales(ptr);
     }
-    cu.advance(a);
+    cu.advance(a, 2);
     lookup();
-    for (uint32_t t = 0; (int64_t)t < tiles; ++t) {
-      const uint32_t bi = t & 1u;
-      if (t >= 2 && !pg_wait_warp(kv_free + bi, ((t >> 1) - 1) & 1u, kErrWaitSmemEmpty)) break;
+    PgWalk w;
+    uint32_t t0 = 0, seg = 0;          // tiles before the item, items with tiles before it
+    bool ok = true;
+    for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
+    if (w.take == 0) continue;
+    ok = pg_stage_q<FP4>(a, w, S.q + g * kPgQBlk, tbase, warp, lane, g, [&]() {
+      const bool k = seg == 0 || pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty);
+      tc_fence_after();
+      return k;
+    });
+    if (!ok) break;
+    if (lane == 0) mbar_arrive(q_full);
+    ++seg;
+    uint32_t t = t0 + ((t0 ^ (uint32_t)g) & 1u);
+    t0 += (uint32_t)w.take;
+    for (; t < t0; t += 2) {
+      const uint32_t bi = t % kPgBufs;
+      if (t >= kPgBufs && !pg_wait_warp(kv_free + bi, (t / kPgBufs - 1) & 1u, kErrWaitSmemEmpty)) {
+        ok = false;
+        break;
+      }
       uint8_t* kt = S.kv + bi * kPgKVBytes;
       if (FP4) {
         const int l16 = lane & 15, kb = l16 >> 1;
@@ -722,7 +767,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
           }
         }
       }
-      if (lane == 0) reinterpret_cast<uint8_t*>(S.valid)[8 * bi + wq] = (uint8_t)vb;
+      if (lane == 0) reinterpret_cast<uint8_t*>(S.valid)[4 * bi + wq] = (uint8_t)vb;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(kv_full + bi);
@@ -733,8 +778,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
       for (int k = 0; k < kN; ++k) r[k] = load_word(ptr, k);
       sc = load_scales(ptr);
-      cu.advance(a);
+      cu.advance(a, 2);
       lookup();
+    }
     }
   } else {
     // ------------------------------------------------------ softmax, output
@@ -747,15 +793,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     bool ok = true;
     int64_t meta_row0 = 0;
     int meta_rows = 0, meta_cont = 0, meta_done = 0;
-    bool go = w.begin(a, S.start);
-    // Q of an item is staged as soon as the one before has its last S read
-    auto stage = [&](const PgWalk& x) {
-      pg_stage_q<FP4>(a, x, S, trow, warp, lane);
-      if (lane == 0) mbar_arrive(q_full);
-    };
-    if (go && w.tiles() > 0) stage(w);
-    while (go) {
-      const int nt = w.tiles();
+    for (bool go = w.begin(a, S.start); go; go = w.next(a)) {
+      const int nt = w.take;
       const int n_rows = w.s.n * a.H - w.j * kPgRows;
       const int ri = w.j * kPgRows + rr;
       // positions this row sees: (lo, hi]; none for rows past the sequence
@@ -763,33 +802,33 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       const int lo = a.window && hi >= a.window ? hi - a.window : -1;
       float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's entry half
       for (int i = 0; i < nt; ++i, ++t) {
-        const uint32_t bi = t & 1u;
-        const int kb = w.k0 + (w.off + i) * kPgE + 32 * part;
+        const uint32_t bi = t % kPgBufs, si = t & 1u;
+        const int kb = w.k0 + (w.off + i) * kPgE + 16 * part;
         // a failed wait leaves `ok` false and skips the later waits; every
         // warp still passes the group's barriers once per tile
-        ok = ok && pg_wait_warp(kv_full + bi, (t >> 1) & 1u, kErrWaitTmaFull);
-        uint32_t mask = S.valid[2 * bi + part];
+        ok = ok && pg_wait_warp(kv_full + bi, (t / kPgBufs) & 1u, kErrWaitTmaFull);
+        uint32_t mask = (S.valid[bi] >> (16 * part)) & 0xFFFFu;
         const int nh = hi - kb + 1, nl = lo - kb + 1;        // entries [nl, nh) of this half
-        mask &= nh >= 32 ? 0xffffffffu : nh <= 0 ? 0u : (1u << nh) - 1u;
-        mask &= nl <= 0 ? 0xffffffffu : nl >= 32 ? 0u : ~((1u << nl) - 1u);
-        ok = ok && pg_wait_warp(s_full, t & 1u, kErrWaitAccFull);
+        mask &= nh >= 16 ? 0xFFFFu : nh <= 0 ? 0u : (1u << nh) - 1u;
+        mask &= nl <= 0 ? 0xFFFFu : nl >= 16 ? 0u : ~((1u << nl) - 1u);
+        ok = ok && pg_wait_warp(s_full + si, (t >> 1) & 1u, kErrWaitAccFull);
         tc_fence_after();
-        uint32_t sv[32];
-        tmem_ld32(trow + kPgSCol + 32 * part, sv);
+        uint32_t sv[16];
+        tmem_ld16(trow + kPgSCol + kPgE * si + 16 * part, sv);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
+        if (lane == 0) mbar_arrive(s_free + si);
         float mt = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) mt = fmaxf(mt, ((mask >> k) & 1u) ? __uint_as_float(sv[k]) : -INFINITY);
+        for (int k = 0; k < 16; ++k) mt = fmaxf(mt, ((mask >> k) & 1u) ? __uint_as_float(sv[k]) : -INFINITY);
         if (mt != -INFINITY) mt *= sc;
-        S.mx[(2 * bi + part) * 64 + rr] = mt;
+        S.mx[(2 * si + part) * 64 + rr] = mt;
         uint32_t over;
         asm volatile("{\n .reg .pred q, r;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred r, 1, 128, q;\n selp.u32 %0, 1, 0, r;\n}"
                      : "=r"(over) : "r"(mt > m_run + kPgRescale ? 1u : 0u) : "memory");
         if (over) {
-          const float mm = fmaxf(mt, S.mx[(2 * bi + (part ^ 1)) * 64 + rr]);
+          const float mm = fmaxf(mt, S.mx[(2 * si + (part ^ 1)) * 64 + rr]);
           float alpha = 1.f;
           if (mm > m_run + kPgRescale) {
             alpha = m_run == -INFINITY ? 0.f : pg_ex2(m_run - mm);
@@ -799,7 +838,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
           if (i > 0) {
             if (part == 0) S.alpha[rr] = alpha;
             named_bar(1, 128);
-            ok = ok && pg_wait_warp(o_done, (t - 1) & 1u, kErrWaitAccFull);
+            // the PV before this tile's has retired (its tile's buffer is free)
+            ok = ok && pg_wait_warp(kv_free + (t - 1) % kPgBufs, ((t - 1) / kPgBufs) & 1u, kErrWaitAccFull);
             tc_fence_after();
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {      // 16 rows at a time
@@ -820,13 +860,13 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
             tmem_wait_st();
           }
         }
-        // the P buffer is free once the PV two tiles back has retired
-        if (t >= 2) ok = ok && pg_wait_warp(kv_free + bi, ((t >> 1) - 1) & 1u, kErrWaitSmemEmpty);
+        // this tile's P buffer is free: its entries were decoded after the PV
+        // that read both last
         const float mref = m_run - kPgPExp;
         float ls = 0.f;
         uint8_t* pt = S.p + bi * kPgPBytes;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -836,7 +876,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
             ls += x0 + x1;
             o[k] = pg_h2u(__floats2half2_rn(x0, x1));
           }
-          *reinterpret_cast<uint4*>(pt + sw128_offset_h(rr, 32 * part + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(pt + sw64_offset(rr, 32 * part + 16 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
         l_run += ls;
         fence_proxy_async_smem();
@@ -844,11 +884,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + bi);
       }
-      PgWalk nx = w;
-      go = nx.next(a);
-      if (go && nx.tiles() > 0) stage(nx);
       // ------------------------------------------------------------ output
-      const bool whole = w.take == w.units;
+      const bool whole = w.take == w.total;
       S.lx[64 * part + rr] = l_run;
       named_bar(1, 128);
       const int64_t orow = (int64_t)w.s.row0 * a.H + w.j * kPgRows;
@@ -874,8 +911,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         }
       }
       named_bar(1, 128);
-      // every PV of the item.  Not o_done: a parity wait cannot tell phases two
-      // apart, and the last two PVs may both be out
+      // every PV of the item
       if (nt > 0) ok = ok && pg_wait_warp(acc_done, seg++ & 1u, kErrWaitAccFull);
       tc_fence_after();
 #pragma unroll 1
@@ -908,7 +944,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
           const int odd = d & 1;
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            const float v0 = __uint_as_float(o[k]) * S.scl[k0 + k], v1 = __uint_as_float(o[k + 1]) * S.scl[k0 + k + 1];
+            const float2 f = *reinterpret_cast<const float2*>(S.scl + k0 + k);
+            const float v0 = __uint_as_float(o[k]) * f.x, v1 = __uint_as_float(o[k + 1]) * f.y;
             const float u = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 2);
             if (k0 + k + odd < n_rows)
               *reinterpret_cast<__nv_bfloat162*>(ob + (int64_t)(k + odd) * kD) =
@@ -925,13 +962,12 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       if (!whole) {
         if (w.off > 0) {
           meta_cont = 1;
-          meta_done = w.off + w.take == w.units;
+          meta_done = w.off + w.take == w.total;
         } else {
           meta_rows = min(n_rows, kPgRows);
           meta_row0 = orow;
         }
       }
-      w = nx;
     }
     if (tid == 0) p.meta[blockIdx.x] = PgMeta{meta_row0, meta_rows, meta_cont, meta_done, 0};
   }
@@ -998,7 +1034,7 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
              rope_out4(make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f), cs, 4 * threadIdx.x));
 }
 
-// CTAs of a call: one per SM, fewer when the call cannot have that many units.
+// CTAs of a call: one per SM, fewer when the call cannot have that many tiles.
 static int pg_grid(const csa_paged_attn_args* a) {
   const int64_t items = (a->n_rows * a->H + kPgRows - 1) / kPgRows + a->kv.B;
   const int64_t tiles = ((int64_t)a->kv.max_pages * a->kv.page_size + kPgE - 1) / kPgE;
