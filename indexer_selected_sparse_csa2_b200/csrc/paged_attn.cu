@@ -8,9 +8,8 @@
 //   S  = Q K^T    tcgen05.mma kind::f16, M = 128 TMEM lanes holding the 64
 //                 rows twice (lane L: row L mod 64), N = 32 entries, K = 512.
 //                 Channels 0..383 of Q are the A operand in TMEM, the last
-//                 128 in shared memory.  The two copies let four softmax
-//                 warps share a tile: warps 0-1 take entries 0..15 of rows
-//                 0..63, warps 2-3 entries 16..31.
+//                 128 in shared memory.  The two copies let two pairs of
+//                 softmax warps take turns: warps 0-1 even tiles, 2-3 odd ones.
 //   O^T += V^T P^T  M = 128 latent channels (4 chunks), N = 64 rows, K = 32
 //                 entries: 4 x 64 TMEM columns, where O (64 x 512) would take
 //                 all 512.  The shared-memory tile of decoded entries is the
@@ -89,9 +88,9 @@ struct PgSmem {
   uint8_t* q;        // channels 384..511 of Q: 2 blocks of 128 rows
   uint8_t* kv;       // [kPgBufs] entry tiles
   uint8_t* p;        // [kPgBufs] P tiles
-  float* mx;         // [2][2][64] tile maxima by tile parity and entry half
+  float* mx;         // [2][64] tile maxima by tile parity
   float* alpha;      // [64] rescale factors
-  float* lx;         // [2][64] sums of the entry halves
+  float* lx;         // [2][64] sums over the even and the odd tiles
   float* scl;        // [64] output factors
   uint32_t* valid;   // [kPgBufs] entries present in a tile
   int64_t* start;    // this CTA's range: {its start inside its first item, length, sequence, item}
@@ -536,9 +535,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   const PgSmem S = carve_pg(smem_raw);
   uint64_t* kv_full = S.bars + 0;    // [kPgBufs] tile decoded (4 warp arrivals)
   uint64_t* kv_free = S.bars + 4;    // [kPgBufs] PV done: entry tile and P tile reusable
-  uint64_t* p_full = S.bars + 8;     // [kPgBufs] P written, O^T rescaled (4 warp arrivals)
+  uint64_t* p_full = S.bars + 8;     // [kPgBufs] P written, O^T rescaled (2 warp arrivals)
   uint64_t* s_full = S.bars + 12;    // [2] S in TMEM
-  uint64_t* s_free = S.bars + 14;    // [2] S read by the softmax (4 warp arrivals)
+  uint64_t* s_free = S.bars + 14;    // [2] S read by the softmax (2 warp arrivals)
   uint64_t* q_full = S.bars + 16;    // an item's Q staged (8 warp arrivals)
   uint64_t* q_free = S.bars + 17;    // an item's last S done
   uint64_t* acc_done = S.bars + 18;  // an item's last PV done
@@ -549,11 +548,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     for (int k = 0; k < kPgBufs; ++k) {
       mbar_init(kv_full + k, 4);
       mbar_init(kv_free + k, 1);
-      mbar_init(p_full + k, 4);
+      mbar_init(p_full + k, 2);
     }
     for (int k = 0; k < 2; ++k) {
       mbar_init(s_full + k, 1);
-      mbar_init(s_free + k, 4);
+      mbar_init(s_free + k, 2);
       mbar_init(drain + k, 1);
     }
     mbar_init(q_full, kPgDeqWarps);
@@ -707,6 +706,20 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     if (!ok) break;
     if (lane == 0) mbar_arrive(q_full);
     ++seg;
+    {
+      // the next item's rows into L2 (an item's rows are contiguous when the
+      // heads are): 128 bytes a thread and step, half a row's two lines a group
+      PgWalk nx = w;
+      if (nx.next(a) && nx.take > 0) {
+        const int nr = min(nx.s.n * a.H - nx.j * kPgRows, kPgRows);
+        for (int l = 32 * (warp & 3) + lane; l < 4 * nr; l += 128) {
+          const int ri = nx.j * kPgRows + (l >> 2), tok = ri / a.H;
+          const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(nx.s.row0 + tok) * a.q_row_stride +
+                                   (int64_t)(ri - tok * a.H) * a.q_head_stride + 64 * (4 * g + (l & 3));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+        }
+      }
+    }
     uint32_t t = t0 + ((t0 ^ (uint32_t)g) & 1u);
     t0 += (uint32_t)w.take;
     for (; t < t0; t += 2) {
@@ -784,8 +797,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     }
   } else {
     // ------------------------------------------------------ softmax, output
+    // Warps 0-1 take the CTA's even tiles, warps 2-3 the odd ones: while one
+    // pair turns its S into P, the other reads the next S and finds its max.
+    // All four meet once per tile, where the running max may move.
     const int rr = 32 * (warp & 1) + lane;     // row of the item
-    const int part = warp >> 1;                // entry half
+    const uint32_t grp = (uint32_t)warp >> 1;
     const uint32_t trow = tbase + ((uint32_t)(32 * warp) << 16);
     const float sc = p.scale_log2;
     PgWalk w;
@@ -800,35 +816,42 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       // positions this row sees: (lo, hi]; none for rows past the sequence
       const int hi = rr < n_rows ? w.s.kv - w.s.n + ri / a.H : -1;
       const int lo = a.window && hi >= a.window ? hi - a.window : -1;
-      float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's entry half
+      float m_run = -INFINITY, l_run = 0.f;    // l_run: this pair's tiles
       for (int i = 0; i < nt; ++i, ++t) {
         const uint32_t bi = t % kPgBufs, si = t & 1u;
-        const int kb = w.k0 + (w.off + i) * kPgE + 16 * part;
+        const bool own = si == grp;
+        uint32_t sv[32], mask = 0;
+        float mt = -INFINITY;
         // a failed wait leaves `ok` false and skips the later waits; every
         // warp still passes the group's barriers once per tile
-        ok = ok && pg_wait_warp(kv_full + bi, (t / kPgBufs) & 1u, kErrWaitTmaFull);
-        uint32_t mask = (S.valid[bi] >> (16 * part)) & 0xFFFFu;
-        const int nh = hi - kb + 1, nl = lo - kb + 1;        // entries [nl, nh) of this half
-        mask &= nh >= 16 ? 0xFFFFu : nh <= 0 ? 0u : (1u << nh) - 1u;
-        mask &= nl <= 0 ? 0xFFFFu : nl >= 16 ? 0u : ~((1u << nl) - 1u);
-        ok = ok && pg_wait_warp(s_full + si, (t >> 1) & 1u, kErrWaitAccFull);
-        tc_fence_after();
-        uint32_t sv[16];
-        tmem_ld16(trow + kPgSCol + kPgE * si + 16 * part, sv);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free + si);
-        float mt = -INFINITY;
+        if (own) {
+          const int kb = w.k0 + (w.off + i) * kPgE;
+          const int nh = hi - kb + 1, nl = lo - kb + 1;      // the row sees entries [nl, nh) of the tile
+          mask = nh >= 32 ? 0xffffffffu : nh <= 0 ? 0u : (1u << nh) - 1u;
+          mask &= nl <= 0 ? 0xffffffffu : nl >= 32 ? 0u : ~((1u << nl) - 1u);
+          ok = ok && pg_wait_warp(s_full + si, (t >> 1) & 1u, kErrWaitAccFull);
+          tc_fence_after();
+          tmem_ld32(trow + kPgSCol + kPgE * si, sv);
+          mask &= S.valid[bi];                 // written before the tile's S was issued
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + si);
+          if (__all_sync(0xffffffffu, mask == 0xffffffffu)) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) mt = fmaxf(mt, ((mask >> k) & 1u) ? __uint_as_float(sv[k]) : -INFINITY);
-        if (mt != -INFINITY) mt *= sc;
-        S.mx[(2 * si + part) * 64 + rr] = mt;
+            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, __uint_as_float(sv[k]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mt = fmaxf(mt, ((mask >> k) & 1u) ? __uint_as_float(sv[k]) : -INFINITY);
+          }
+          if (mt != -INFINITY) mt *= sc;
+          S.mx[64 * si + rr] = mt;
+        }
         uint32_t over;
         asm volatile("{\n .reg .pred q, r;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred r, 1, 128, q;\n selp.u32 %0, 1, 0, r;\n}"
                      : "=r"(over) : "r"(mt > m_run + kPgRescale ? 1u : 0u) : "memory");
         if (over) {
-          const float mm = fmaxf(mt, S.mx[(2 * si + (part ^ 1)) * 64 + rr]);
+          const float mm = S.mx[64 * si + rr];
           float alpha = 1.f;
           if (mm > m_run + kPgRescale) {
             alpha = m_run == -INFINITY ? 0.f : pg_ex2(m_run - mm);
@@ -836,7 +859,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
             l_run *= alpha;
           }
           if (i > 0) {
-            if (part == 0) S.alpha[rr] = alpha;
+            if (own) S.alpha[rr] = alpha;
             named_bar(1, 128);
             // the PV before this tile's has retired (its tile's buffer is free)
             ok = ok && pg_wait_warp(kv_free + (t - 1) % kPgBufs, ((t - 1) / kPgBufs) & 1u, kErrWaitAccFull);
@@ -858,39 +881,49 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
               }
             }
             tmem_wait_st();
+            tc_fence_before();
+            named_bar(1, 128);                 // every quarter rescaled before this tile's PV
           }
         }
-        // this tile's P buffer is free: its entries were decoded after the PV
-        // that read both last
-        const float mref = m_run - kPgPExp;
-        float ls = 0.f;
-        uint8_t* pt = S.p + bi * kPgPBytes;
+        if (own) {
+          // this tile's P buffer is free: its entries were decoded after the
+          // PV that read both last
+          const float mref = m_run - kPgPExp;
+          float l0 = 0.f, l1 = 0.f;
+          uint8_t* pt = S.p + bi * kPgPBytes;
+          const bool full = __all_sync(0xffffffffu, mask == 0xffffffffu);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t o[4];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e0 = 8 * c + 2 * k;
-            const float x0 = ((mask >> e0) & 1u) ? pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref)) : 0.f;
-            const float x1 = ((mask >> (e0 + 1)) & 1u) ? pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref)) : 0.f;
-            ls += x0 + x1;
-            o[k] = pg_h2u(__floats2half2_rn(x0, x1));
+            for (int k = 0; k < 4; ++k) {
+              const int e0 = 8 * c + 2 * k;
+              float x0 = pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref));
+              float x1 = pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref));
+              if (!full) {
+                x0 = ((mask >> e0) & 1u) ? x0 : 0.f;
+                x1 = ((mask >> (e0 + 1)) & 1u) ? x1 : 0.f;
+              }
+              l0 += x0;
+              l1 += x1;
+              o[k] = pg_h2u(__floats2half2_rn(x0, x1));
+            }
+            *reinterpret_cast<uint4*>(pt + sw64_offset(rr, 16 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          *reinterpret_cast<uint4*>(pt + sw64_offset(rr, 32 * part + 16 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+          l_run += l0 + l1;
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + bi);
         }
-        l_run += ls;
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + bi);
       }
       // ------------------------------------------------------------ output
       const bool whole = w.take == w.total;
-      S.lx[64 * part + rr] = l_run;
+      S.lx[64 * grp + rr] = l_run;
       named_bar(1, 128);
       const int64_t orow = (int64_t)w.s.row0 * a.H + w.j * kPgRows;
       const int slot = 2 * blockIdx.x + (w.off > 0 ? 0 : 1);
-      if (part == 0) {
+      if (grp == 0) {
         float l = l_run + S.lx[64 + rr];
         if (whole) {
           const float m0 = m_run - kPgPExp;
@@ -940,22 +973,35 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
           }
           // rows k, k + 1: the lane of the even channel stores row k's pair of
           // channels, the lane of the odd one row k + 1's
-          __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + (orow + k0) * kD + (d & ~1);
           const int odd = d & 1;
+          __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + (orow + k0 + odd) * kD + (d & ~1);
+          uint32_t v[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float2 f = *reinterpret_cast<const float2*>(S.scl + k0 + k);
-            const float v0 = __uint_as_float(o[k]) * f.x, v1 = __uint_as_float(o[k + 1]) * f.y;
+          for (int k = 0; k < 16; ++k) {
+            const float2 f = *reinterpret_cast<const float2*>(S.scl + k0 + 2 * k);
+            const float v0 = __uint_as_float(o[2 * k]) * f.x, v1 = __uint_as_float(o[2 * k + 1]) * f.y;
             const float u = __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 2);
-            if (k0 + k + odd < n_rows)
-              *reinterpret_cast<__nv_bfloat162*>(ob + (int64_t)(k + odd) * kD) =
-                  odd ? __floats2bfloat162_rn(u, v1) : __floats2bfloat162_rn(v0, u);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(odd ? u : v0, odd ? v1 : u);
+            v[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          if (k0 + 32 <= n_rows) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) *reinterpret_cast<uint32_t*>(ob + 2 * k * kD) = v[k];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (k0 + 2 * k + odd < n_rows) *reinterpret_cast<uint32_t*>(ob + 2 * k * kD) = v[k];
           }
         } else {
           float* po = p.part_o + (int64_t)slot * (64 * kD) + k0 * kD + d;
+          if (k0 + 32 <= n_rows) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (k0 + k < n_rows) po[k * kD] = __uint_as_float(o[k]);
+            for (int k = 0; k < 32; ++k) po[k * kD] = __uint_as_float(o[k]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k0 + k < n_rows) po[k * kD] = __uint_as_float(o[k]);
+          }
         }
       }
       tc_fence_before();
