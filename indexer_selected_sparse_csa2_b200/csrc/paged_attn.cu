@@ -55,7 +55,7 @@ constexpr int kPgRows = 128;              // query rows per item (two CTAs)
 constexpr int kPgHalf = 64;               // ... per CTA
 constexpr int kPgE = 64;                  // entries per key tile
 constexpr int kPgOwn = 32;                // ... decoded by one CTA
-constexpr int kPgKBufs = 2, kPgVBufs = 4; // K and V tiles in flight
+constexpr int kPgKBufs = 2, kPgVBufs = 3; // K and V tiles in flight
 constexpr int kPgWarpDec = 4;             // first decode warp (two groups of 4)
 constexpr int kPgWarpS = 12;
 constexpr int kPgWarpPV = 13;
@@ -98,6 +98,7 @@ struct PgMeta {
 struct PgParams {
   csa_paged_attn_args a;
   float scale_log2;  // softmax_scale * log2(e)
+  uint32_t page_inv; // floor(2^32 / page_size), 2^32 - 1 for 1
   float* part_o;     // [2 * pairs][128][512] fp32
   float2* part_ml;   // [2 * pairs][128] (max, sum)
   PgMeta* meta;      // [pairs]
@@ -686,8 +687,14 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       if (cu.live) {
         const int pos = cu.w.k0 + (cu.w.off + cu.i) * kPgE + e_at;
         if (pos < cu.w.k1) {
-          const uint32_t pg = (uint32_t)pos / (uint32_t)a.kv.page_size;
+          // pos / page_size: the product with floor(2^32 / page_size) is at
+          // most one short for pos < 2^31
+          uint32_t pg = __umulhi((uint32_t)pos, p.page_inv);
           slot = (uint32_t)pos - pg * (uint32_t)a.kv.page_size;
+          if (slot >= (uint32_t)a.kv.page_size) {
+            ++pg;
+            slot -= (uint32_t)a.kv.page_size;
+          }
           id = a.kv.block_table[(int64_t)cu.w.b * a.kv.table_stride + pg];
         }
       }
@@ -698,13 +705,6 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     uint4 r[kN], x[kN / 2];
     uint2 sc, scx;
     uint32_t vb;                       // valid entries: 8 own, 8 of the other half
-    // address of lane l's entry; where there is none, the cache's first entry:
-    // every load is issued, and the decoder writes zeros
-    auto entry_ptr = [&](uint32_t& v) -> unsigned long long {
-      const bool on = id >= 0 && id < a.kv.n_pages;
-      v = __ballot_sync(0xffffffffu, on) & 0xFFFFu;
-      return (unsigned long long)(a.kv.pages + (on ? (int64_t)id * a.kv.page_stride + (int64_t)slot * a.kv.row_stride : 0));
-    };
     auto at_lane = [&](unsigned long long ptr, int l) {
       return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, ptr, l));
     };
@@ -717,25 +717,49 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     const int xb = FP4 ? (lane & 7) >> 1 : (lane & 15) >> 2;
     const int xc = (xb >> 1) * 4 + 2 * (int)rank + (xb & 1);
     const int x_off = FP4 ? 32 * xc + 16 * (lane & 1) : 64 * xc + 16 * (lane & 3);
-    auto load_tile = [&](unsigned long long ptr) {
+    // All loads of a tile.  Where there is no entry, the cache's first one is
+    // read instead, and the decoder writes zeros.
+    auto load_tile = [&]() {
+      const bool on = id >= 0 && id < a.kv.n_pages;
+      vb = __ballot_sync(0xffffffffu, on) & 0xFFFFu;
+      const unsigned long long ptr =
+          (unsigned long long)(a.kv.pages + (on ? (int64_t)id * a.kv.page_stride + (int64_t)slot * a.kv.row_stride : 0));
+      const uint8_t *q0, *q1;          // the entries whose scales this lane loads
+      const int id0 = __shfl_sync(0xffffffffu, id, lane & 8);
+      if (__all_sync(0xffffffffu, on && id == id0)) {
+        // the usual case: a warp's 8 entries of either half lie in one page,
+        // so their addresses need no exchange (a load behind each pair of
+        // shuffles made these 14 loads take 2000 cycles)
+        const int64_t rs = a.kv.row_stride;
+        const uint8_t *p0 = at_lane(ptr, 0), *p1 = at_lane(ptr, 8);
+        q0 = p0 + (lane >> 2) * rs;
+        q1 = p1 + (lane >> 2) * rs;
+        const uint8_t* o = p0 + (FP4 ? (lane >> 4) * rs + 16 * (lane & 15) : 16 * lane);
 #pragma unroll
-      for (int k = 0; k < kN; ++k)
-        r[k] = ld_nc_v4(at_lane(ptr, FP4 ? 2 * k + (lane >> 4) : k) + 16 * (FP4 ? lane & 15 : lane));
+        for (int k = 0; k < kN; ++k, o += (FP4 ? 2 : 1) * rs) r[k] = ld_nc_v4(o);
+        o = p1 + (FP4 ? lane >> 3 : lane >> 4) * rs + x_off;
 #pragma unroll
-      for (int k = 0; k < kN / 2; ++k) x[k] = ld_nc_v4(at_lane(ptr, 8 + (FP4 ? 4 * k + (lane >> 3) : 2 * k + (lane >> 4))) + x_off);
-      // scales: lane 4e + w holds word w of entry e's scale bytes
-      const uint8_t* q0 = at_lane(ptr, lane >> 2) + kScaleOff;
-      const uint8_t* q1 = at_lane(ptr, 8 + (lane >> 2)) + kScaleOff;
-      if (FP4) {
-        sc = *reinterpret_cast<const uint2*>(q0 + 8 * (lane & 3));
-        scx = *reinterpret_cast<const uint2*>(q1 + 8 * (lane & 3));
+        for (int k = 0; k < kN / 2; ++k, o += (FP4 ? 4 : 2) * rs) x[k] = ld_nc_v4(o);
       } else {
-        sc.x = *reinterpret_cast<const uint32_t*>(q0 + 4 * (lane & 3));
-        scx.x = *reinterpret_cast<const uint32_t*>(q1 + 4 * (lane & 3));
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+          r[k] = ld_nc_v4(at_lane(ptr, FP4 ? 2 * k + (lane >> 4) : k) + 16 * (FP4 ? lane & 15 : lane));
+#pragma unroll
+        for (int k = 0; k < kN / 2; ++k) x[k] = ld_nc_v4(at_lane(ptr, 8 + (FP4 ? 4 * k + (lane >> 3) : 2 * k + (lane >> 4))) + x_off);
+        q0 = at_lane(ptr, lane >> 2);
+        q1 = at_lane(ptr, 8 + (lane >> 2));
+      }
+      // scales: lane 4e + w holds word w of entry e's scale bytes
+      if (FP4) {
+        sc = *reinterpret_cast<const uint2*>(q0 + kScaleOff + 8 * (lane & 3));
+        scx = *reinterpret_cast<const uint2*>(q1 + kScaleOff + 8 * (lane & 3));
+      } else {
+        sc.x = *reinterpret_cast<const uint32_t*>(q0 + kScaleOff + 4 * (lane & 3));
+        scx.x = *reinterpret_cast<const uint32_t*>(q1 + kScaleOff + 4 * (lane & 3));
       }
     };
     lookup();
-    load_tile(entry_ptr(vb));
+    load_tile();
     cu.advance(a, 2);
     lookup();
     const bool v_own = (uint32_t)((kb >> 1) & 1) == rank;   // block kb belongs to this CTA's V
@@ -867,7 +891,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         // the next tile's entries, all loads together (issued one by one
         // between the decodes, each decode waits for the load before it: loads
         // share their scoreboards), then the table values of the tile after it
-        load_tile(entry_ptr(vb));
+        load_tile();
         cu.advance(a, 2);
         lookup();
       }
@@ -877,7 +901,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     const int q4 = warp, rr = 32 * (q4 & 1) + lane;          // TMEM lane quarter, row of this CTA
     const int half = q4 >> 1;                                // entries 32 half .. of a tile; channel half of a block
     const uint32_t trow = tbase + ((uint32_t)(32 * q4) << 16);
-    const float sc = p.scale_log2;
+    // scale 0: logits 0 with factor 1, since -inf * 0 is not a number
+    const bool zero = p.scale_log2 == 0.f;
+    const float sc = zero ? 1.f : p.scale_log2;
     const uint32_t s_free_at = dsmem(s_free, 0), p_full_at = dsmem(p_full, 0);
     PgWalk w;
     uint32_t t = 0, seg = 0;
@@ -909,8 +935,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         tc_fence_before();
         __syncwarp();
         if (lane == 0) pg_arrive(s_free_at + 8 * si);
-        const bool full = __all_sync(0xffffffffu, mask == 0xffffffffu);
-        if (!full) {
+        if (zero) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sv[k] = 0u;
+        }
+        if (!__all_sync(0xffffffffu, mask == 0xffffffffu)) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) sv[k] = ((mask >> k) & 1u) ? sv[k] : 0xff800000u;   // -inf
         }
@@ -962,14 +991,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int e0 = 8 * c + 2 * k;
-            float x0, x1;
-            if (sc > 0.f || full) {
-              x0 = pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref));
-              x1 = pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref));
-            } else {                           // scale 0: -inf * 0 is not a number
-              x0 = sv[e0] == 0xff800000u ? 0.f : pg_ex2(-mref);
-              x1 = sv[e0 + 1] == 0xff800000u ? 0.f : pg_ex2(-mref);
-            }
+            const float x0 = pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref));
+            const float x1 = pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref));
             l0 += x0;
             l1 += x1;
             o[k] = pg_h2u(__floats2half2_rn(x0, x1));
@@ -1163,6 +1186,7 @@ cudaError_t launch_paged_attn(const csa_paged_attn_args* a, void* ws, cudaStream
   PgParams p;
   p.a = *a;
   p.scale_log2 = a->softmax_scale * kPgLog2e;
+  p.page_inv = a->kv.page_size == 1 ? 0xffffffffu : (uint32_t)(((uint64_t)1 << 32) / (uint32_t)a->kv.page_size);
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.meta = reinterpret_cast<PgMeta*>(w);
   w += pg_al256((size_t)g * sizeof(PgMeta));
