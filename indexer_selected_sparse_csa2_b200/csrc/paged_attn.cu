@@ -61,7 +61,6 @@ constexpr int kPgWarpS = 12;
 constexpr int kPgWarpPV = 13;
 constexpr int kPgWarps = 14;
 constexpr int kPgThreads = 32 * kPgWarps;
-constexpr int kPgSoftThreads = 128;
 constexpr int kPgQTmemBlocks = 6;         // 64-channel blocks of Q in TMEM
 constexpr int kPgQBlk = kPgHalf * 128;    // shared Q block: 64 rows x 64 fp16
 constexpr int kPgKBlk = kPgOwn * 128;     // 64-channel block of a K tile
@@ -943,14 +942,18 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
           for (int k = 0; k < 32; ++k) sv[k] = ((mask >> k) & 1u) ? sv[k] : 0xff800000u;   // -inf
         }
-        float mt = -INFINITY;
+        float m4[4];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) mt = fmaxf(mt, __uint_as_float(sv[k]));
+        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(__uint_as_float(sv[k]), __uint_as_float(sv[k + 4]));
+#pragma unroll
+        for (int k = 8; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(sv[k]));
+        float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         if (mt != -INFINITY) mt *= sc;
         S.mx[(2 * si + half) * 64 + rr] = mt;
         uint32_t over;
-        asm volatile("{\n .reg .pred q, r;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred r, 1, 128, q;\n selp.u32 %0, 1, 0, r;\n}"
-                     : "=r"(over) : "r"(mt > m_run + kPgRescale ? 1u : 0u) : "memory");
+        // a row's two halves are lanes of warps w and w + 2: they meet here
+        asm volatile("{\n .reg .pred q, r;\n setp.ne.u32 q, %2, 0;\n bar.red.or.pred r, %1, 64, q;\n selp.u32 %0, 1, 0, r;\n}"
+                     : "=r"(over) : "r"(1 + (q4 & 1)), "r"(mt > m_run + kPgRescale ? 1u : 0u) : "memory");
         if (over) {
           const float mm = fmaxf(mt, S.mx[(2 * si + (half ^ 1)) * 64 + rr]);
           float alpha = 1.f;
@@ -1008,7 +1011,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       // ------------------------------------------------------------ output
       const bool whole = w.take == w.total;
       S.lx[half * 64 + rr] = l_run;
-      named_bar(1, kPgSoftThreads);
+      named_bar(1 + (q4 & 1), 64);
       const float l = S.lx[rr] + S.lx[64 + rr];
       const int64_t orow = (int64_t)w.s.row0 * a.H + w.j * kPgRows + R.base;
       const int slot = 2 * pair + (w.off > 0 ? 0 : 1);
@@ -1029,7 +1032,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       } else if (warp < 2 && rr < R.on) {
         p.part_ml[slot * kPgRows + R.base + rr] = make_float2(m_run, l);
       }
-      named_bar(1, kPgSoftThreads);            // lx read
+      named_bar(1 + (q4 & 1), 64);            // lx read
       // every PV of the item
       if (nt > 0) ok = ok && pg_wait_warp(acc_done, seg++ & 1u, kErrWaitAccFull);
       tc_fence_after();
