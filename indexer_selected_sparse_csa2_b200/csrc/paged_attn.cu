@@ -177,6 +177,10 @@ CSA_DEV void pg_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t ides
       " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n}"
       ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "n"(ACC ? 1 : 0) : "memory");
 }
+CSA_DEV void pg_st32(void* p, const uint32_t* v) {   // 32 bytes, aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
 CSA_DEV bool pg_elect() {
   uint32_t e;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
@@ -451,65 +455,42 @@ struct PgRowsOf {
   }
 };
 
-// Stages half g of this CTA's query rows of an item: channels 192 g ..
-// 192 g + 191 into TMEM (twice: lanes L and L + 64 hold row L), channels
-// 384 + 64 g .. into shared block g.  Called by the 4 warps of decode group g;
-// rows past the item's are zero.  The first loads are issued before the wait
-// for the operand's last reader.
+// Stages channels 256 g .. of this CTA's query rows of an item, by the 4 warps
+// of decode group g: channels below 384 into TMEM (twice: lanes L and L + 64
+// hold row L), the last 128 into the shared blocks.  A warp reads whole rows
+// (512 bytes an instruction; a row a lane would touch 32 lines each) and the
+// rows for TMEM change hands through the group's K tile, which is free: every
+// S of the item before is done.  Rows past the item's are zero.
+// `wait` waits for the operand's last reader; after a failed one (false) the
+// warps only keep their barriers.
 template <typename Wait>
-CSA_DEV bool pg_stage_q(const csa_paged_attn_args& a, const PgWalk& w, const PgRowsOf& R, uint8_t* qblk, uint32_t tbase, int warp,
-                        int lane, int g, Wait wait) {
-  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q);
+CSA_DEV void pg_stage_q(const csa_paged_attn_args& a, const PgWalk& w, const PgRowsOf& R, const PgSmem& S, uint32_t tbase, int wl,
+                        int lane, int g, bool& ok, Wait wait) {
+  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + 256 * g + 8 * lane;
   const int r0 = w.j * kPgRows + R.base;
-  auto q_row = [&](int rr) -> const __nv_bfloat16* {
-    const int ri = r0 + rr, tok = ri / a.H;
-    return qb + (int64_t)(w.s.row0 + tok) * a.q_row_stride + (int64_t)(ri - tok * a.H) * a.q_head_stride;
-  };
-  const int wl = warp & 3, rr = (32 * wl + lane) & 63;
-  const bool on = rr < R.on;
-  const uint4* src = reinterpret_cast<const uint4*>(q_row(on ? rr : 0)) + 24 * g;
-  bool ok = true;
+  uint8_t* buf = S.k + g * kPgKBytes;                      // [64 rows][512 bytes], 16-byte chunk c of row r at c ^ (r & 31)
 #pragma unroll 1
-  for (int u = 0; u < 3; ++u) {                            // 32 columns: 64 channels
-    uint4 v[8];
+  for (int u = 0; u < 4 && ok; ++u) {                      // 4 rows of the warp's 16
+    uint4 v[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = on ? src[8 * u + k] : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < 4; ++k) {
+      const int rr = 16 * wl + 4 * u + k, ri = r0 + rr, tok = ri / a.H;
+      v[k] = rr < R.on ? *reinterpret_cast<const uint4*>(qb + (int64_t)(w.s.row0 + tok) * a.q_row_stride +
+                                                         (int64_t)(ri - tok * a.H) * a.q_head_stride)
+                       : make_uint4(0, 0, 0, 0);
+    }
     if (u == 0) {
       ok = wait();
       if (!ok) break;
     }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t o[16];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float f[8];
-        pg_bf16x8(v[4 * q + k], f);
-        const uint4 h = pg_f16x8(f);
-        o[4 * k] = h.x;
-        o[4 * k + 1] = h.y;
-        o[4 * k + 2] = h.z;
-        o[4 * k + 3] = h.w;
-      }
-      tmem_st16(tbase + ((uint32_t)(32 * wl) << 16) + 96u * g + 32u * u + 16u * q, o);
-    }
-  }
-  if (ok) {
-    const int st = 32 * wl + lane, c8 = st & 7;            // 128 threads: 16 rows x 8 chunks, 4 times
-    uint4 v[4];
-#pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int r = (st >> 3) + 16 * k;
-      v[k] = r < R.on ? *reinterpret_cast<const uint4*>(q_row(r) + 384 + 64 * g + 8 * c8) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = (st >> 3) + 16 * k;
+      const int rr = 16 * wl + 4 * u + k;
       float f[8];
       pg_bf16x8(v[k], f);
-      if (a.rope_cs && g == 1 && r < R.on) {               // channels 448 + 8 c8 ..
-        const int tok = w.s.row0 + (r0 + r) / a.H;
-        const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * c8);
+      if (a.rope_cs && g == 1 && lane >= 24 && rr < R.on) {  // channels 448 + 8 (lane - 24) ..
+        const int tok = w.s.row0 + (r0 + rr) / a.H;
+        const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * (lane - 24));
         const float4 ca = cs[0], cb = cs[1];
         float2 x;
         x = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = x.x; f[1] = x.y;
@@ -517,14 +498,32 @@ CSA_DEV bool pg_stage_q(const csa_paged_attn_args& a, const PgWalk& w, const PgR
         x = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = x.x; f[5] = x.y;
         x = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = x.x; f[7] = x.y;
       }
-      *reinterpret_cast<uint4*>(qblk + sw128_offset_h(r, 8 * c8)) = pg_f16x8(f);
+      uint8_t* to = g == 1 && lane >= 16 ? S.q + ((lane - 16) >> 3) * kPgQBlk + sw128_offset_h(rr, 8 * (lane & 7))
+                                         : buf + rr * 512 + 16 * (lane ^ (rr & 31));
+      *reinterpret_cast<uint4*>(to) = pg_f16x8(f);
+    }
+  }
+  named_bar(4 + g, 128);
+  if (ok) {
+    const int rr = (32 * wl + lane) & 63;
+    const uint8_t* from = buf + rr * 512;
+    for (int c = 0; c < (g ? 16 : 32); c += 4) {           // 16 columns
+      uint32_t o[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 h = *reinterpret_cast<const uint4*>(from + 16 * ((c + k) ^ (rr & 31)));
+        o[4 * k] = h.x;
+        o[4 * k + 1] = h.y;
+        o[4 * k + 2] = h.z;
+        o[4 * k + 3] = h.w;
+      }
+      tmem_st16(tbase + ((uint32_t)(32 * wl) << 16) + 128u * g + 4u * c, o);
     }
     tmem_wait_st();
     fence_proxy_async_smem();
     tc_fence_before();
   }
-  __syncwarp();
-  return ok;
+  named_bar(4 + g, 128);                                   // the K tile is read
 }
 
 // A position in the pair's list of key tiles.
@@ -553,27 +552,29 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const PgSmem S = carve_pg(smem_raw);
   // Waited on in CTA 0, whose warps issue for both; arrivals from both CTAs:
-  uint64_t* kv_full = S.bars + 0;    // [kPgVBufs] tile decoded (8 warp arrivals)
-  uint64_t* s_free = S.bars + 4;     // [2] S read by the softmax (8)
-  uint64_t* p_full = S.bars + 6;     // [2] P written, O rescaled (8)
-  uint64_t* q_full = S.bars + 8;     // an item's Q staged (16)
+  uint64_t* k_full = S.bars + 0;     // [kPgKBufs] K tile decoded (8 warp arrivals)
+  uint64_t* v_full = S.bars + 2;     // [kPgVBufs] V tile decoded (8)
+  uint64_t* s_free = S.bars + 6;     // [2] S read by the softmax (8)
+  uint64_t* p_full = S.bars + 8;     // [2] P written, O rescaled (8)
+  uint64_t* q_full = S.bars + 10;    // an item's Q staged (16)
   // In both CTAs, by commits:
-  uint64_t* k_free = S.bars + 9;     // [kPgKBufs] S done: K tile reusable
-  uint64_t* v_free = S.bars + 11;    // [kPgVBufs] PV done: V tile (and P tile) reusable
-  uint64_t* s_full = S.bars + 15;    // [2] S in TMEM
-  uint64_t* q_free = S.bars + 17;    // an item's last S done
-  uint64_t* acc_done = S.bars + 18;  // an item's last PV done
-  uint64_t* drain = S.bars + 19;     // [2] all MMAs of an issuer retired (teardown)
+  uint64_t* k_free = S.bars + 11;    // [kPgKBufs] S done: K tile reusable
+  uint64_t* v_free = S.bars + 13;    // [kPgVBufs] PV done: V tile (and P tile) reusable
+  uint64_t* s_full = S.bars + 17;    // [2] S in TMEM
+  uint64_t* q_free = S.bars + 19;    // an item's last S done
+  uint64_t* acc_done = S.bars + 20;  // an item's last PV done
+  uint64_t* drain = S.bars + 21;     // [2] all MMAs of an issuer retired (teardown)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const csa_paged_attn_args& a = p.a;
   if (tid == 0) {
     for (int k = 0; k < kPgVBufs; ++k) {
-      mbar_init(kv_full + k, 8);
+      mbar_init(v_full + k, 8);
       mbar_init(v_free + k, 1);
     }
     for (int k = 0; k < 2; ++k) {
+      mbar_init(k_full + k, 8);
       mbar_init(k_free + k, 1);
       mbar_init(s_full + k, 1);
       mbar_init(s_free + k, 8);
@@ -608,8 +609,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         if (w.take == 0) continue;
         ok = pg_wait_warp(q_full, seg++ & 1u, kErrWaitTmaFull);
         for (int i = 0; i < w.take && ok; ++i, ++t) {
-          const uint32_t vi = t % kPgVBufs, si = t & 1u;
-          ok = pg_wait_warp(kv_full + vi, (t / kPgVBufs) & 1u, kErrWaitTmaFull);
+          const uint32_t si = t & 1u;
+          ok = pg_wait_warp(k_full + t % kPgKBufs, (t / kPgKBufs) & 1u, kErrWaitTmaFull);
           if (ok && t >= 2) ok = pg_wait_warp(s_free + si, ((t >> 1) - 1) & 1u, kErrWaitAccEmpty);
           if (!ok) break;
           tc_fence_after();
@@ -642,7 +643,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       bool ok = true;
       for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
         for (int i = 0; i < w.take; ++i, ++t) {
-          ok = pg_wait_warp(p_full + (t & 1u), (t >> 1) & 1u, kErrWaitAccFull);
+          ok = pg_wait_warp(v_full + t % kPgVBufs, (t / kPgVBufs) & 1u, kErrWaitTmaFull);
+          ok = ok && pg_wait_warp(p_full + (t & 1u), (t >> 1) & 1u, kErrWaitAccFull);
           if (!ok) break;
           tc_fence_after();
           const uint32_t vd = vd0 + (t % kPgVBufs) * (kPgVBytes >> 4), pd = pd0 + (t & 1u) * (kPgPBytes >> 4);
@@ -765,22 +767,23 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     const uint32_t k_at = smem_u32(S.k) + (uint32_t)kb * kPgKBlk;
     const uint32_t v_at = smem_u32(S.v) + (uint32_t)((kb >> 2) * 2 + (kb & 1)) * kPgVBlk + kPgOwn * 128 * rank;
     const uint32_t x_at = smem_u32(S.v) + (uint32_t)xb * kPgVBlk + kPgOwn * 128 * (rank ^ 1u);
-    const uint32_t full_at = dsmem(kv_full, 0), q_full_at = dsmem(q_full, 0);
+    const uint32_t k_full_at = dsmem(k_full, 0), v_full_at = dsmem(v_full, 0), q_full_at = dsmem(q_full, 0);
     auto st16 = [](uint32_t at, const uint4& q) {
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
     };
     PgWalk w;
     uint32_t t0 = 0, seg = 0;          // tiles before the item, items with tiles before it
     bool ok = true;
-    for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
+    // a failed wait leaves `ok` false and skips the later waits and all work;
+    // every warp still passes its group's barriers once per item
+    for (bool go = w.begin(a, S.start); go; go = w.next(a)) {
       if (w.take == 0) continue;
-      ok = pg_stage_q(a, w, PgRowsOf(a, w, rank), S.q + g * kPgQBlk, tbase, warp, lane, g, [&]() {
+      pg_stage_q(a, w, PgRowsOf(a, w, rank), S, tbase, wq, lane, g, ok, [&]() {
         const bool k = seg == 0 || pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty);
         tc_fence_after();
         return k;
       });
-      if (!ok) break;
-      if (lane == 0) pg_arrive(q_full_at);
+      if (ok && lane == 0) pg_arrive(q_full_at);
       ++seg;
       {
         // the next item's rows into L2: 128 bytes a thread and step
@@ -799,15 +802,22 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       t0 += (uint32_t)w.take;
       for (; t < t0; t += 2) {
         const uint32_t vi = t % kPgVBufs;
-        if (t >= kPgKBufs) ok = pg_wait_warp(k_free + t % kPgKBufs, (t / kPgKBufs - 1) & 1u, kErrWaitSmemEmpty);
+        if (ok && t >= kPgKBufs) ok = pg_wait_warp(k_free + t % kPgKBufs, (t / kPgKBufs - 1) & 1u, kErrWaitSmemEmpty);
         if (ok && t >= kPgVBufs) ok = pg_wait_warp(v_free + vi, (t / kPgVBufs - 1) & 1u, kErrWaitSmemEmpty);
-        if (!ok) break;
+        if (!ok) continue;
         const uint32_t kt = k_at + (t % kPgKBufs) * kPgKBytes, vt = v_at + vi * kPgVBytes, xt = x_at + vi * kPgVBytes;
         auto put = [&](int row, int c, const uint4& q) {    // 8 channels of an own entry
           const uint32_t o = sw128_offset_h(row, c);
           st16(kt + o, q);
           if (v_own) st16(vt + o, q);
         };
+        // K is announced before the other half's V is decoded: S can start.
+        auto announce = [&](uint32_t bar) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) pg_arrive(bar);
+        };
+        if (lane < 2) reinterpret_cast<uint8_t*>(S.valid)[8 * vi + 4 * (rank ^ (uint32_t)lane) + wq] = (uint8_t)(vb >> (8 * lane));
         // Stores go in an order by block, so that 8 lanes' stores meet 8
         // different 16-byte columns.
         if (FP4) {
@@ -824,6 +834,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
             for (int m = 0; m < 4; ++m) put(8 * wq + e, 32 * (l16 & 1) + 8 * (m ^ (kb & 3)), c[m]);
           }
+          announce(k_full_at + 8 * (t % kPgKBufs));
 #pragma unroll
           for (int k = 0; k < kN / 2; ++k) {
             // this lane's 32 channels: scale bytes 4 xc + 2 (lane & 1), + 1
@@ -859,6 +870,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
               put(8 * wq + k, 16 * (lane & 3) + 8 * f, pg_decode_fp8(r[k].x, r[k].y, m));
               put(8 * wq + k, 16 * (lane & 3) + 8 * (f ^ 1), pg_decode_fp8(r[k].z, r[k].w, m));
             }
+            announce(k_full_at + 8 * (t % kPgKBufs));
 #pragma unroll
             for (int k = 0; k < kN / 2; ++k) {
               const int e = 2 * k + (lane >> 4);
@@ -874,6 +886,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
               put(8 * wq + k, 16 * (lane & 3), pg_decode_fp8_far(r[k].x, r[k].y, m));
               put(8 * wq + k, 16 * (lane & 3) + 8, pg_decode_fp8_far(r[k].z, r[k].w, m));
             }
+            announce(k_full_at + 8 * (t % kPgKBufs));
 #pragma unroll
             for (int k = 0; k < kN / 2; ++k) {
               const int e = 2 * k + (lane >> 4);
@@ -883,10 +896,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
             }
           }
         }
-        if (lane < 2) reinterpret_cast<uint8_t*>(S.valid)[8 * vi + 4 * (rank ^ (uint32_t)lane) + wq] = (uint8_t)(vb >> (8 * lane));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) pg_arrive(full_at + 8 * vi);
+        announce(v_full_at + 8 * vi);
         // the next tile's entries, all loads together (issued one by one
         // between the decodes, each decode waits for the load before it: loads
         // share their scoreboards), then the table values of the tile after it
@@ -1038,6 +1048,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       tc_fence_after();
       // this lane's row, channels 128 half .. + 127 of each 256
       const bool valid_o = nt > 0 && ok;
+      const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // whole sectors (a row is 1 KB)
       const float2* cs = nullptr;
       if (whole && a.rope_cs && half == 1 && rr < R.on)
         cs = reinterpret_cast<const float2*>(a.rope_cs + (int64_t)(w.s.row0 + ri / a.H) * 64);
@@ -1066,20 +1077,22 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
               f[2 * k + 1] = y.y;
             }
           }
+          uint32_t h[16];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t h[4];
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+            h[k] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          if (out32) {
+            pg_st32(ob + ch, h);
+            pg_st32(ob + ch + 16, h + 8);
+          } else {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[8 * k + 2 * m], f[8 * k + 2 * m + 1]);
-              h[m] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            *reinterpret_cast<uint4*>(ob + ch + 8 * k) = make_uint4(h[0], h[1], h[2], h[3]);
+            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(ob + ch + 8 * k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
           }
         } else if (rr < R.on) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(po + ch + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 4; ++k) pg_st32(po + ch + 8 * k, o + 8 * k);
         }
         __syncwarp();
       }
@@ -1111,19 +1124,21 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   }
 }
 
-// Joins the partials of the items that several pairs share.  CTA (i, r): row r
-// of the item that pair i of the attention began and did not finish; its
-// partials are slot 2i + 1 and then slot 2k of k = i + 1, i + 2, ... up to
-// the pair that ends the item, added in that order.
+// Joins the partials of the items that several pairs share.  CTA (i, y): rows
+// y, y + kPgCombRows, ... of the item that pair i of the attention began and
+// did not finish; its partials are slot 2i + 1 and then slot 2k of
+// k = i + 1, i + 2, ... up to the pair that ends the item, added in that order.
+constexpr int kPgCombRows = 32;
 __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PgParams p, int n_pairs) {
   pdl_enter();
   const csa_paged_attn_args& a = p.a;
-  const int i = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31;
+  const int i = blockIdx.x, lane = threadIdx.x & 31;
   const PgMeta me = p.meta[i];
-  if (row >= me.rows) return;
+  if ((int)blockIdx.y >= me.rows) return;
   int n = 1;                                   // partials
   for (int k0 = i + 1; k0 < n_pairs; k0 += 32) {
-    const uint32_t end = __ballot_sync(0xffffffffu, k0 + lane < n_pairs && p.meta[k0 + lane].cont && p.meta[k0 + lane].done);
+    const PgMeta mk = k0 + lane < n_pairs ? p.meta[k0 + lane] : PgMeta{0, 0, 0, 0, 0};
+    const uint32_t end = __ballot_sync(0xffffffffu, mk.cont && mk.done);
     if (end) {
       n = k0 - i + __ffs(end);
       break;
@@ -1131,39 +1146,41 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
     n = min(k0 + 32, n_pairs) - i;
   }
   auto slot = [&](int s) { return (int64_t)(s == 0 ? 2 * i + 1 : 2 * (i + s)); };
-  const int64_t orow = me.row0 + row;
-  const int head = (int)(orow % a.H);
-  const float s0 = a.sink ? a.sink[head] * kPgLog2e : -INFINITY;
-  float M = -INFINITY;
-  for (int s = lane; s < n; s += 32) M = fmaxf(M, p.part_ml[slot(s) * kPgRows + row].x);
-  M = warp_max(M);
-  M = fmaxf(M - kPgPExp, s0);
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* po = p.part_o + (int64_t)row * kD + 4 * threadIdx.x;
-  for (int sb = 0; sb < n; sb += 32) {
-    float wt = 0.f;
-    if (sb + lane < n) {
-      const float2 ml = p.part_ml[slot(sb + lane) * kPgRows + row];
-      wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - kPgPExp - M);
-      L += wt * ml.y;
-    }
-    const int m = min(32, n - sb);
+  for (int row = blockIdx.y; row < me.rows; row += kPgCombRows) {
+    const int64_t orow = me.row0 + row;
+    const int head = (int)(orow % a.H);
+    const float s0 = a.sink ? a.sink[head] * kPgLog2e : -INFINITY;
+    float M = -INFINITY;
+    for (int s = lane; s < n; s += 32) M = fmaxf(M, p.part_ml[slot(s) * kPgRows + row].x);
+    M = warp_max(M);
+    M = fmaxf(M - kPgPExp, s0);
+    float L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* po = p.part_o + (int64_t)row * kD + 4 * threadIdx.x;
+    for (int sb = 0; sb < n; sb += 32) {
+      float wt = 0.f;
+      if (sb + lane < n) {
+        const float2 ml = p.part_ml[slot(sb + lane) * kPgRows + row];
+        wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - kPgPExp - M);
+        L += wt * ml.y;
+      }
+      const int m = min(32, n - sb);
 #pragma unroll 8
-    for (int s = 0; s < m; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, wt, s);
-      const float4 v = *reinterpret_cast<const float4*>(po + slot(sb + s) * (kPgRows * kD));
-      acc.x += ws * v.x; acc.y += ws * v.y; acc.z += ws * v.z; acc.w += ws * v.w;
+      for (int s = 0; s < m; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, wt, s);
+        const float4 v = *reinterpret_cast<const float4*>(po + slot(sb + s) * (kPgRows * kD));
+        acc.x += ws * v.x; acc.y += ws * v.y; acc.z += ws * v.z; acc.w += ws * v.w;
+      }
     }
+    L = warp_sum(L);
+    const bool any = L > 0.f;
+    if (s0 != -INFINITY) L += exp2f(s0 - M);
+    const float f = any ? 1.f / L : 0.f;
+    if (threadIdx.x == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kPgLn2 : -INFINITY;
+    const float* cs = a.rope_cs ? a.rope_cs + orow / a.H * 64 : nullptr;
+    store_out4(a.out, true, orow * kD + 4 * threadIdx.x,
+               rope_out4(make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f), cs, 4 * threadIdx.x));
   }
-  L = warp_sum(L);
-  const bool any = L > 0.f;
-  if (s0 != -INFINITY) L += exp2f(s0 - M);
-  const float f = any ? 1.f / L : 0.f;
-  if (threadIdx.x == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kPgLn2 : -INFINITY;
-  const float* cs = a.rope_cs ? a.rope_cs + orow / a.H * 64 : nullptr;
-  store_out4(a.out, true, orow * kD + 4 * threadIdx.x,
-             rope_out4(make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f), cs, 4 * threadIdx.x));
 }
 
 // CTA pairs of a call: one per two SMs, fewer when the call cannot have that
@@ -1217,7 +1234,7 @@ cudaError_t launch_paged_attn(const csa_paged_attn_args* a, void* ws, cudaStream
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(stream, "paged_attn_combine");
-    launch_k(paged_attn_combine_kernel, dim3(g, kPgRows), dim3(128), 0, stream, p, g);
+    launch_k(paged_attn_combine_kernel, dim3(g, kPgCombRows), dim3(128), 0, stream, p, g);
   }
   note_launches(2);
   return cudaGetLastError();
