@@ -358,7 +358,7 @@ csa_status csa_paged_append(const csa_paged_append_args* a, csa_stream_t stream)
 typedef struct {
   csa_paged_kv kv;
   const void* q;             /* bf16, row i head h at q + i*q_row_stride + h*q_head_stride elements */
-  int64_t n_rows;            /* rows of q and out, >= cu_q[B]; n_rows * H < 2^31 */
+  int64_t n_rows;            /* rows of q and out, >= cu_q[B]; n_rows * H < 2^30 */
   int64_t q_row_stride;      /* elements, multiples of 8 */
   int64_t q_head_stride;     /* elements, >= 512, a multiple of 8 */
   int32_t H, D;              /* H in 1..128; D must be 512 */

@@ -198,7 +198,7 @@ static csa_status check_paged_attn(const csa_paged_attn_args* a) {
   const csa_status s = check_paged(&a->kv);
   if (s != CSA_OK) return s;
   if (a->H < 1 || a->H > 128 || a->D != kD || a->window < 0) return CSA_ERR_SHAPE;
-  if (a->n_rows < 0 || a->n_rows * (int64_t)a->H >= ((int64_t)1 << 31) || a->n_rows >= ((int64_t)1 << 31)) return CSA_ERR_SHAPE;
+  if (a->n_rows < 0 || a->n_rows >= ((int64_t)1 << 31) || a->n_rows * a->H >= ((int64_t)1 << 30)) return CSA_ERR_SHAPE;
   if (a->n_rows == 0) return CSA_OK;
   if (!a->q || !a->out) return CSA_ERR_INVALID_ARG;
   if (!(a->softmax_scale >= 0.f) || !(a->softmax_scale <= 3.0e38f)) return CSA_ERR_INVALID_ARG;

@@ -97,7 +97,7 @@ struct PgMeta {
 struct PgParams {
   csa_paged_attn_args a;
   float scale_log2;  // softmax_scale * log2(e)
-  uint32_t page_inv; // floor(2^32 / page_size), 2^32 - 1 for 1
+  uint32_t page_inv, h_inv;   // pg_inv of page_size and H
   float* part_o;     // [2 * pairs][128][512] fp32
   float2* part_ml;   // [2 * pairs][128] (max, sum)
   PgMeta* meta;      // [pairs]
@@ -190,6 +190,23 @@ CSA_DEV bool pg_elect() {
 constexpr uint32_t kPgIdescS = (1u << 4) | ((uint32_t)(kPgE >> 3) << 17) | ((uint32_t)(kPgRows >> 4) << 24);
 constexpr uint32_t kPgIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(kPgRows >> 4) << 24);
 
+// n / d for 0 <= n < 2^31: the product with floor(2^32 / d) is at most one short
+// (d = 1: with 2^32 - 1).
+static uint32_t pg_inv(uint32_t d) { return d == 1 ? 0xffffffffu : (uint32_t)(((uint64_t)1 << 32) / d); }
+CSA_DEV int pg_div(int n, int d, uint32_t inv, int& rem) {
+  uint32_t q = __umulhi((uint32_t)n, inv), r = (uint32_t)n - q * (uint32_t)d;
+  if (r >= (uint32_t)d) {
+    ++q;
+    r -= (uint32_t)d;
+  }
+  rem = (int)r;
+  return (int)q;
+}
+CSA_DEV int pg_div(int n, int d, uint32_t inv) {
+  int r;
+  return pg_div(n, d, inv, r);
+}
+
 // ------------------------------------------------------------- work items --
 struct PgSeq {
   int n;        // new tokens
@@ -208,9 +225,10 @@ CSA_DEV PgSeq pg_seq(const csa_paged_attn_args& a, int b) {
 }
 // Positions [k0, k1) that the rows of item j see (k1 = k0: none), before the
 // rows' own masks.  Row r of the item is (token, head) row 128 j + r.
-CSA_DEV void pg_item(const csa_paged_attn_args& a, const PgSeq& s, int j, int& k0, int& k1) {
+CSA_DEV void pg_item(const PgParams& p, const PgSeq& s, int j, int& k0, int& k1) {
+  const csa_paged_attn_args& a = p.a;
   const int r0 = j * kPgRows, r1 = min(r0 + kPgRows, s.n * a.H) - 1;
-  const int p0 = s.kv - s.n + r0 / a.H, p1 = s.kv - s.n + r1 / a.H;
+  const int p0 = s.kv - s.n + pg_div(r0, a.H, p.h_inv), p1 = s.kv - s.n + pg_div(r1, a.H, p.h_inv);
   k1 = min(p1 + 1, a.kv.max_pages * a.kv.page_size);
   k0 = a.window ? max(0, p0 + 1 > a.window ? p0 + 1 - a.window : 0) : 0;
   if (k1 < k0) k1 = k0;
@@ -226,8 +244,8 @@ struct PgWalk {
   PgSeq s;
   int k0, k1, total;   // the item's positions and key tiles
   int off, take;       // first key tile taken here, number taken
-  CSA_DEV void item(const csa_paged_attn_args& a) {
-    pg_item(a, s, j, k0, k1);
+  CSA_DEV void item(const PgParams& p) {
+    pg_item(p, s, j, k0, k1);
     total = pg_tiles(k0, k1);
     off = min(max(at - kPgItemCost, 0), total);
     take = (int)min((int64_t)total, max(at + left - kPgItemCost, (int64_t)0)) - off;
@@ -235,36 +253,36 @@ struct PgWalk {
   // does this pair do anything for the item? (a tileless one belongs to the
   // pair at its start)
   CSA_DEV bool mine() const { return take > 0 || (total == 0 && at == 0); }
-  CSA_DEV void settle(const csa_paged_attn_args& a) {
-    while (left > 0 && !mine()) step(a);
+  CSA_DEV void settle(const PgParams& p) {
+    while (left > 0 && !mine()) step(p);
   }
-  CSA_DEV void step(const csa_paged_attn_args& a) {
+  CSA_DEV void step(const PgParams& p) {
     left -= kPgItemCost + total - at;
     at = 0;
     if (left <= 0) return;
     if (++j >= s.tiles) {
       j = 0;
       do {
-        if (++b >= a.kv.B) { left = 0; return; }
-        s = pg_seq(a, b);
+        if (++b >= p.a.kv.B) { left = 0; return; }
+        s = pg_seq(p.a, b);
       } while (s.tiles == 0);
     }
-    item(a);
+    item(p);
   }
-  CSA_DEV bool begin(const csa_paged_attn_args& a, const int64_t* start) {
+  CSA_DEV bool begin(const PgParams& p, const int64_t* start) {
     at = (int)start[0];
     left = start[1];
     b = (int)start[2];
     j = (int)start[3];
     if (left <= 0) return false;
-    s = pg_seq(a, b);
-    item(a);
-    settle(a);
+    s = pg_seq(p.a, b);
+    item(p);
+    settle(p);
     return left > 0;
   }
-  CSA_DEV bool next(const csa_paged_attn_args& a) {
-    step(a);
-    settle(a);
+  CSA_DEV bool next(const PgParams& p) {
+    step(p);
+    settle(p);
     return left > 0;
   }
 };
@@ -276,7 +294,8 @@ CSA_DEV int64_t pg_warp_sum64(int64_t v) {
 }
 // Cost of sequences 32 g + lane (0 past the last).  Sequences with many
 // items are summed by the whole warp.
-CSA_DEV int64_t pg_group_cost(const csa_paged_attn_args& a, int g, int lane) {
+CSA_DEV int64_t pg_group_cost(const PgParams& p, int g, int lane) {
+  const csa_paged_attn_args& a = p.a;
   const int b = 32 * g + lane;
   PgSeq s{0, 0, 0, 0};
   if (b < a.kv.B) s = pg_seq(a, b);
@@ -284,7 +303,7 @@ CSA_DEV int64_t pg_group_cost(const csa_paged_attn_args& a, int g, int lane) {
   if (s.tiles <= 4) {
     for (int j = 0; j < s.tiles; ++j) {
       int k0, k1;
-      pg_item(a, s, j, k0, k1);
+      pg_item(p, s, j, k0, k1);
       u += kPgItemCost + pg_tiles(k0, k1);
     }
   }
@@ -298,7 +317,7 @@ CSA_DEV int64_t pg_group_cost(const csa_paged_attn_args& a, int g, int lane) {
     int64_t v = 0;
     for (int j = lane; j < q.tiles; j += 32) {
       int k0, k1;
-      pg_item(a, q, j, k0, k1);
+      pg_item(p, q, j, k0, k1);
       v += kPgItemCost + pg_tiles(k0, k1);
     }
     v = pg_warp_sum64(v);
@@ -322,11 +341,12 @@ CSA_DEV int pg_locate(int64_t v, int64_t& at, int lane) {
 }
 // Finds the range of the cost axis of pair `pair` of `pairs`; every warp of a
 // CTA takes part, both CTAs find the same.
-CSA_DEV void pg_plan(const csa_paged_attn_args& a, const PgSmem& S, int pair, int pairs, int warp, int lane) {
+CSA_DEV void pg_plan(const PgParams& p, const PgSmem& S, int pair, int pairs, int warp, int lane) {
+  const csa_paged_attn_args& a = p.a;
   int64_t* gsum = reinterpret_cast<int64_t*>(S.v);
   const int groups = (a.kv.B + 31) / 32;
   for (int g = warp; g < groups; g += kPgWarps) {
-    const int64_t u = pg_warp_sum64(pg_group_cost(a, g, lane));
+    const int64_t u = pg_warp_sum64(pg_group_cost(p, g, lane));
     if (lane == 0) gsum[g] = u;
   }
   __syncthreads();
@@ -353,14 +373,14 @@ CSA_DEV void pg_plan(const csa_paged_attn_args& a, const PgSmem& S, int pair, in
         }
         at -= sum;
       }
-      const int64_t v = pg_group_cost(a, base, lane);     // the sequence
+      const int64_t v = pg_group_cost(p, base, lane);     // the sequence
       b = 32 * base + pg_locate(v, at, lane);
       const PgSeq s = pg_seq(a, b);
       for (;; j += 32) {                                   // the item
         int64_t w = 0;
         if (j + lane < s.tiles) {
           int k0, k1;
-          pg_item(a, s, j + lane, k0, k1);
+          pg_item(p, s, j + lane, k0, k1);
           w = kPgItemCost + pg_tiles(k0, k1);
         }
         const int64_t sum = pg_warp_sum64(w);
@@ -457,67 +477,76 @@ struct PgRowsOf {
 
 // Stages channels 256 g .. of this CTA's query rows of an item, by the 4 warps
 // of decode group g: channels below 384 into TMEM (twice: lanes L and L + 64
-// hold row L), the last 128 into the shared blocks.  A warp reads whole rows
-// (512 bytes an instruction; a row a lane would touch 32 lines each) and the
-// rows for TMEM change hands through the group's K tile, which is free: every
-// S of the item before is done.  Rows past the item's are zero.
-// `wait` waits for the operand's last reader; after a failed one (false) the
-// warps only keep their barriers.
+// hold row L), the last 128 into the shared blocks, all as fp16.  The rows
+// come as they are, by asynchronous copies of whole rows (a row a lane would
+// touch 32 lines an instruction), into the group's K tile, which is free:
+// every S of the item before is done.  Rows past the item's are zero.
+// `wait` waits for that; after a failed wait (false) the warps only keep their
+// barriers.
+CSA_DEV void pg_cp_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
 template <typename Wait>
-CSA_DEV void pg_stage_q(const csa_paged_attn_args& a, const PgWalk& w, const PgRowsOf& R, const PgSmem& S, uint32_t tbase, int wl,
+CSA_DEV void pg_stage_q(const PgParams& p, const PgWalk& w, const PgRowsOf& R, const PgSmem& S, uint32_t tbase, int wl,
                         int lane, int g, bool& ok, Wait wait) {
-  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + 256 * g + 8 * lane;
+  const csa_paged_attn_args& a = p.a;
   const int r0 = w.j * kPgRows + R.base;
   uint8_t* buf = S.k + g * kPgKBytes;                      // [64 rows][512 bytes], 16-byte chunk c of row r at c ^ (r & 31)
-#pragma unroll 1
-  for (int u = 0; u < 4 && ok; ++u) {                      // 4 rows of the warp's 16
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int rr = 16 * wl + 4 * u + k, ri = r0 + rr, tok = ri / a.H;
-      v[k] = rr < R.on ? *reinterpret_cast<const uint4*>(qb + (int64_t)(w.s.row0 + tok) * a.q_row_stride +
-                                                         (int64_t)(ri - tok * a.H) * a.q_head_stride)
-                       : make_uint4(0, 0, 0, 0);
-    }
-    if (u == 0) {
-      ok = wait();
-      if (!ok) break;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int rr = 16 * wl + 4 * u + k;
-      float f[8];
-      pg_bf16x8(v[k], f);
-      if (a.rope_cs && g == 1 && lane >= 24 && rr < R.on) {  // channels 448 + 8 (lane - 24) ..
-        const int tok = w.s.row0 + (r0 + rr) / a.H;
-        const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * (lane - 24));
-        const float4 ca = cs[0], cb = cs[1];
-        float2 x;
-        x = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = x.x; f[1] = x.y;
-        x = rope_fwd(f[2], f[3], ca.z, ca.w); f[2] = x.x; f[3] = x.y;
-        x = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = x.x; f[5] = x.y;
-        x = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = x.x; f[7] = x.y;
+  if (ok) ok = wait();
+  if (ok) {
+    const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + 256 * g + 8 * lane;
+    int head, tok = pg_div(r0 + 16 * wl, a.H, p.h_inv, head) + w.s.row0;
+    const uint32_t at = smem_u32(buf) + 16 * wl * 512;
+#pragma unroll 4
+    for (int k = 0; k < 16; ++k) {                         // the warp's 16 rows
+      const bool on = 16 * wl + k < R.on;
+      pg_cp_async16(at + k * 512 + 16 * (lane ^ ((16 * wl + k) & 31)),
+                    on ? qb + (int64_t)tok * a.q_row_stride + (int64_t)head * a.q_head_stride : qb, on);
+      if (++head == a.H) {
+        head = 0;
+        ++tok;
       }
-      uint8_t* to = g == 1 && lane >= 16 ? S.q + ((lane - 16) >> 3) * kPgQBlk + sw128_offset_h(rr, 8 * (lane & 7))
-                                         : buf + rr * 512 + 16 * (lane ^ (rr & 31));
-      *reinterpret_cast<uint4*>(to) = pg_f16x8(f);
     }
+    cp_async_commit();
+    cp_async_wait_all();
   }
   named_bar(4 + g, 128);
   if (ok) {
     const int rr = (32 * wl + lane) & 63;
     const uint8_t* from = buf + rr * 512;
+#pragma unroll 2
     for (int c = 0; c < (g ? 16 : 32); c += 4) {           // 16 columns
       uint32_t o[16];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint4 h = *reinterpret_cast<const uint4*>(from + 16 * ((c + k) ^ (rr & 31)));
+        float f[8];
+        pg_bf16x8(*reinterpret_cast<const uint4*>(from + 16 * ((c + k) ^ (rr & 31))), f);
+        const uint4 h = pg_f16x8(f);
         o[4 * k] = h.x;
         o[4 * k + 1] = h.y;
         o[4 * k + 2] = h.z;
         o[4 * k + 3] = h.w;
       }
       tmem_st16(tbase + ((uint32_t)(32 * wl) << 16) + 128u * g + 4u * c, o);
+    }
+    if (g == 1) {
+#pragma unroll 2
+      for (int k = 0; k < 8; ++k) {                        // 8 rows x 16 chunks of the last 128 channels
+        const int r = 8 * k + 2 * wl + (lane >> 4), c = lane & 15;
+        float f[8];
+        pg_bf16x8(*reinterpret_cast<const uint4*>(buf + r * 512 + 16 * ((16 + c) ^ (r & 31))), f);
+        if (a.rope_cs && c >= 8 && r < R.on) {             // channels 448 + 8 (c - 8) ..
+          const int tok = w.s.row0 + pg_div(r0 + r, a.H, p.h_inv);
+          const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * (c - 8));
+          const float4 ca = cs[0], cb = cs[1];
+          float2 x;
+          x = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = x.x; f[1] = x.y;
+          x = rope_fwd(f[2], f[3], ca.z, ca.w); f[2] = x.x; f[3] = x.y;
+          x = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = x.x; f[5] = x.y;
+          x = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = x.x; f[7] = x.y;
+        }
+        *reinterpret_cast<uint4*>(S.q + (c >> 3) * kPgQBlk + sw128_offset_h(r, 8 * (c & 7))) = pg_f16x8(f);
+      }
     }
     tmem_wait_st();
     fence_proxy_async_smem();
@@ -531,16 +560,16 @@ struct PgCursor {
   PgWalk w;
   int i;           // tile of the item
   bool live;
-  CSA_DEV void begin(const csa_paged_attn_args& a, const int64_t* start, int skip) {
-    live = w.begin(a, start);
+  CSA_DEV void begin(const PgParams& p, const int64_t* start, int skip) {
+    live = w.begin(p, start);
     i = 0;
-    advance(a, skip);
+    advance(p, skip);
   }
-  CSA_DEV void advance(const csa_paged_attn_args& a, int n) {
+  CSA_DEV void advance(const PgParams& p, int n) {
     i += n;
     while (live && i >= w.take) {
       i -= w.take;
-      live = w.next(a);
+      live = w.next(p);
     }
   }
 };
@@ -592,7 +621,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  pg_plan(a, S, pair, pairs, warp, lane);
+  pg_plan(p, S, pair, pairs, warp, lane);
   tc_fence_before();
   cluster_sync_all();                // barriers and TMEM of both CTAs are there
   tc_fence_after();
@@ -605,7 +634,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       PgWalk w;
       uint32_t t = 0, seg = 0;
       bool ok = true;
-      for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
+      for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
         if (w.take == 0) continue;
         ok = pg_wait_warp(q_full, seg++ & 1u, kErrWaitTmaFull);
         for (int i = 0; i < w.take && ok; ++i, ++t) {
@@ -641,7 +670,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       PgWalk w;
       uint32_t t = 0;
       bool ok = true;
-      for (bool go = w.begin(a, S.start); go && ok; go = w.next(a)) {
+      for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
         for (int i = 0; i < w.take; ++i, ++t) {
           ok = pg_wait_warp(v_full + t % kPgVBufs, (t / kPgVBufs) & 1u, kErrWaitTmaFull);
           ok = ok && pg_wait_warp(p_full + (t & 1u), (t >> 1) & 1u, kErrWaitAccFull);
@@ -666,6 +695,27 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       }
       if (pg_elect()) pg_commit(drain + 1);
       __syncwarp();
+    } else {
+      // CTA 1's warp fetches the next item's query rows, of both CTAs, into L2
+      // once an item's last S is done
+      PgWalk w;
+      uint32_t seg = 0;
+      bool ok = true;
+      for (bool go = w.begin(p, S.start); go && ok;) {
+        const bool tiles = w.take > 0;
+        go = w.next(p);
+        if (go && w.take > 0) {
+          const int n = min(w.s.n * a.H - w.j * kPgRows, kPgRows);
+          for (int l = lane; l < 8 * n; l += 32) {         // 128 bytes each
+            int head;
+            const int tok = pg_div(w.j * kPgRows + (l >> 3), a.H, p.h_inv, head);
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(w.s.row0 + tok) * a.q_row_stride +
+                                     (int64_t)head * a.q_head_stride + 64 * (l & 7);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+          }
+        }
+        if (go && tiles) ok = pg_wait_warp(q_free, seg++ & 1u, kErrWaitSmemEmpty);
+      }
     }
   } else if (warp >= kPgWarpDec) {
     // ---------------------------------------------- entry loads and decoding
@@ -676,7 +726,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     // 3000 cycles a tile in the fence behind its remote stores.)
     const int wq = (warp - kPgWarpDec) & 3, g = (warp - kPgWarpDec) >> 2;
     PgCursor cu;                       // the tile whose page table values are fetched next
-    cu.begin(a, S.start, g);
+    cu.begin(p, S.start, g);
     // page id and entry number in the page of entry 8 wq + (lane & 7), lanes
     // 8-15 (24-31) of the other CTA's half, of the tile whose entries are
     // loaded next
@@ -688,14 +738,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       if (cu.live) {
         const int pos = cu.w.k0 + (cu.w.off + cu.i) * kPgE + e_at;
         if (pos < cu.w.k1) {
-          // pos / page_size: the product with floor(2^32 / page_size) is at
-          // most one short for pos < 2^31
-          uint32_t pg = __umulhi((uint32_t)pos, p.page_inv);
-          slot = (uint32_t)pos - pg * (uint32_t)a.kv.page_size;
-          if (slot >= (uint32_t)a.kv.page_size) {
-            ++pg;
-            slot -= (uint32_t)a.kv.page_size;
-          }
+          int rem;
+          const int pg = pg_div(pos, a.kv.page_size, p.page_inv, rem);
+          slot = (uint32_t)rem;
           id = a.kv.block_table[(int64_t)cu.w.b * a.kv.table_stride + pg];
         }
       }
@@ -761,7 +806,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     };
     lookup();
     load_tile();
-    cu.advance(a, 2);
+    cu.advance(p, 2);
     lookup();
     const bool v_own = (uint32_t)((kb >> 1) & 1) == rank;   // block kb belongs to this CTA's V
     const uint32_t k_at = smem_u32(S.k) + (uint32_t)kb * kPgKBlk;
@@ -776,28 +821,15 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     bool ok = true;
     // a failed wait leaves `ok` false and skips the later waits and all work;
     // every warp still passes its group's barriers once per item
-    for (bool go = w.begin(a, S.start); go; go = w.next(a)) {
+    for (bool go = w.begin(p, S.start); go; go = w.next(p)) {
       if (w.take == 0) continue;
-      pg_stage_q(a, w, PgRowsOf(a, w, rank), S, tbase, wq, lane, g, ok, [&]() {
+      pg_stage_q(p, w, PgRowsOf(a, w, rank), S, tbase, wq, lane, g, ok, [&]() {
         const bool k = seg == 0 || pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty);
         tc_fence_after();
         return k;
       });
       if (ok && lane == 0) pg_arrive(q_full_at);
       ++seg;
-      {
-        // the next item's rows into L2: 128 bytes a thread and step
-        PgWalk nx = w;
-        if (nx.next(a) && nx.take > 0) {
-          const PgRowsOf R(a, nx, rank);
-          for (int l = 32 * wq + lane; l < 4 * R.on; l += 128) {
-            const int ri = nx.j * kPgRows + R.base + (l >> 2), tok = ri / a.H;
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(nx.s.row0 + tok) * a.q_row_stride +
-                                     (int64_t)(ri - tok * a.H) * a.q_head_stride + 64 * (4 * g + (l & 3));
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
-          }
-        }
-      }
       uint32_t t = t0 + ((t0 ^ (uint32_t)g) & 1u);
       t0 += (uint32_t)w.take;
       for (; t < t0; t += 2) {
@@ -901,7 +933,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         // between the decodes, each decode waits for the load before it: loads
         // share their scoreboards), then the table values of the tile after it
         load_tile();
-        cu.advance(a, 2);
+        cu.advance(p, 2);
         lookup();
       }
     }
@@ -919,12 +951,14 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     bool ok = true;
     int64_t meta_row0 = 0;
     int meta_rows = 0, meta_cont = 0, meta_done = 0;
-    for (bool go = w.begin(a, S.start); go; go = w.next(a)) {
+    for (bool go = w.begin(p, S.start); go; go = w.next(p)) {
       const int nt = w.take;
       const PgRowsOf R(a, w, rank);
       const int ri = w.j * kPgRows + R.base + rr;
       // positions this row sees: (lo, hi]; none for rows past the item's
-      const int hi = rr < R.on ? w.s.kv - w.s.n + ri / a.H : -1;
+      int head;
+      const int tok = pg_div(ri, a.H, p.h_inv, head);
+      const int hi = rr < R.on ? w.s.kv - w.s.n + tok : -1;
       const int lo = a.window && hi >= a.window ? hi - a.window : -1;
       float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's entry half
       for (int i = 0; i < nt; ++i, ++t) {
@@ -1030,7 +1064,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         const float m0 = m_run - kPgPExp;
         float M = m0, L = l;
         if (a.sink) {
-          const float s0 = rr < R.on ? a.sink[ri - ri / a.H * a.H] * kPgLog2e : -INFINITY;
+          const float s0 = rr < R.on ? a.sink[head] * kPgLog2e : -INFINITY;
           M = fmaxf(m0, s0);
           const float f = l > 0.f ? exp2f(m0 - M) : 0.f;
           L = l * f + (s0 == -INFINITY ? 0.f : exp2f(s0 - M));
@@ -1048,51 +1082,70 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       tc_fence_after();
       // this lane's row, channels 128 half .. + 127 of each 256
       const bool valid_o = nt > 0 && ok;
-      const bool out32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // whole sectors (a row is 1 KB)
       const float2* cs = nullptr;
       if (whole && a.rope_cs && half == 1 && rr < R.on)
-        cs = reinterpret_cast<const float2*>(a.rope_cs + (int64_t)(w.s.row0 + ri / a.H) * 64);
-      __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + (orow + rr) * kD + 128 * half;
-      float* po = p.part_o + ((int64_t)slot * kPgRows + R.base + rr) * kD + 128 * half;
+        cs = reinterpret_cast<const float2*>(a.rope_cs + (int64_t)(w.s.row0 + tok) * 64);
+      // A lane's row goes through 128 bytes of the (free) P tiles, so that a
+      // store instruction writes whole lines of four rows instead of a piece
+      // of each of 32.  The warp's 4 KB are touched again by other warps' P
+      // only behind the next tile's meeting of the row's two warps.
+      uint8_t* st = S.p + half * kPgPBytes + (q4 & 1) * 4096;
+      uint8_t* st_row = st + lane * 128;
+      const int8_t sw = (int8_t)(lane & 7);
+      const int rl = lane >> 3, cl = lane & 7;               // row of four, 16-byte chunk
+      const uint8_t* ld_row = st + rl * 128;
+      const int step = whole ? 64 : 32;                      // columns a pass: 128 bytes of bf16 or fp32
+      uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(static_cast<__nv_bfloat16*>(a.out) + orow * kD)
+                           : reinterpret_cast<uint8_t*>(p.part_o + ((int64_t)slot * kPgRows + R.base) * kD);
+      const int64_t row_bytes = whole ? kD * 2 : kD * 4;
+      dst += (32 * (q4 & 1) + rl) * row_bytes + 16 * cl;
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {      // TMEM column; channel c (+ 128 in the second block) of the lane's
-        const int ch = c < 128 ? c : c + 128;
-        uint32_t o[32];
-        if (valid_o) {
-          tmem_ld32(trow + kPgOCol + c, o);
-          tmem_wait_ld();
-        } else {
+      for (int c = 0; c < 256; c += step) {
+        const int ch = c + 128 * half + (c < 128 ? 0 : 128); // first channel
+        if (whole) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0u;
-        }
-        if (rr < R.on && whole) {
-          float f[32];
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[32];
+            if (valid_o) {
+              tmem_ld32(trow + kPgOCol + c + 32 * h, o);
+              tmem_wait_ld();
+            } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) f[k] = __uint_as_float(o[k]) * scl;
-          if (cs && c >= 192) {                // channels 448 + (c - 192) ..
+              for (int k = 0; k < 32; ++k) o[k] = 0u;
+            }
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float2 z = cs[((c - 192) >> 1) + k], y = rope_inv(f[2 * k], f[2 * k + 1], z.x, z.y);
-              f[2 * k] = y.x;
-              f[2 * k + 1] = y.y;
+              float2 f = make_float2(__uint_as_float(o[2 * k]) * scl, __uint_as_float(o[2 * k + 1]) * scl);
+              if (cs && c == 192) {                          // channels 448 + 32 h + 2 k
+                const float2 z = cs[16 * h + k];
+                f = rope_inv(f.x, f.y, z.x, z.y);
+              }
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x, f.y);
+              o[k] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-          }
-          uint32_t h[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-            h[k] = *reinterpret_cast<const uint32_t*>(&b2);
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(st_row + 16 * ((4 * h + k) ^ sw)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
-          if (out32) {
-            pg_st32(ob + ch, h);
-            pg_st32(ob + ch + 16, h + 8);
+        } else {
+          uint32_t o[32];
+          if (valid_o) {
+            tmem_ld32(trow + kPgOCol + c, o);
+            tmem_wait_ld();
           } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(ob + ch + 8 * k) = make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]);
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
-        } else if (rr < R.on) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) pg_st32(po + ch + 8 * k, o + 8 * k);
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(st_row + 16 * (k ^ sw)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        __syncwarp();
+        uint8_t* to = dst + (int64_t)ch * (whole ? 2 : 4);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {                        // rows 4 k + rl of the warp's 32
+          const uint4 v = *reinterpret_cast<const uint4*>(ld_row + 512 * k + 16 * (cl ^ ((4 * k + rl) & 7)));
+          if (32 * (q4 & 1) + 4 * k + rl < R.on) *reinterpret_cast<uint4*>(to + 4 * k * row_bytes) = v;
         }
         __syncwarp();
       }
@@ -1206,7 +1259,8 @@ cudaError_t launch_paged_attn(const csa_paged_attn_args* a, void* ws, cudaStream
   PgParams p;
   p.a = *a;
   p.scale_log2 = a->softmax_scale * kPgLog2e;
-  p.page_inv = a->kv.page_size == 1 ? 0xffffffffu : (uint32_t)(((uint64_t)1 << 32) / (uint32_t)a->kv.page_size);
+  p.page_inv = pg_inv((uint32_t)a->kv.page_size);
+  p.h_inv = pg_inv((uint32_t)a->H);
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.meta = reinterpret_cast<PgMeta*>(w);
   w += pg_al256((size_t)g * sizeof(PgMeta));
