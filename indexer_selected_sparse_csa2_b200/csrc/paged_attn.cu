@@ -1099,6 +1099,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
                            : reinterpret_cast<uint8_t*>(p.part_o + ((int64_t)slot * kPgRows + R.base) * kD);
       const int64_t row_bytes = whole ? kD * 2 : kD * 4;
       dst += (32 * (q4 & 1) + rl) * row_bytes + 16 * cl;
+      const int rows_on = R.on - 32 * (q4 & 1) - rl;
 #pragma unroll 1
       for (int c = 0; c < 256; c += step) {
         const int ch = c + 128 * half + (c < 128 ? 0 : 128); // first channel
@@ -1113,14 +1114,18 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
               for (int k = 0; k < 32; ++k) o[k] = 0u;
             }
+            if (cs && c == 192) {                            // channels 448 + 32 h ..
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float2 z = cs[16 * h + k], f = rope_inv(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]), z.x, z.y);
+                o[2 * k] = __float_as_uint(f.x);
+                o[2 * k + 1] = __float_as_uint(f.y);
+              }
+            }
+            __syncwarp();
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              float2 f = make_float2(__uint_as_float(o[2 * k]) * scl, __uint_as_float(o[2 * k + 1]) * scl);
-              if (cs && c == 192) {                          // channels 448 + 32 h + 2 k
-                const float2 z = cs[16 * h + k];
-                f = rope_inv(f.x, f.y, z.x, z.y);
-              }
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x, f.y);
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * scl, __uint_as_float(o[2 * k + 1]) * scl);
               o[k] = *reinterpret_cast<const uint32_t*>(&b2);
             }
 #pragma unroll
@@ -1145,7 +1150,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < 8; ++k) {                        // rows 4 k + rl of the warp's 32
           const uint4 v = *reinterpret_cast<const uint4*>(ld_row + 512 * k + 16 * (cl ^ ((4 * k + rl) & 7)));
-          if (32 * (q4 & 1) + 4 * k + rl < R.on) *reinterpret_cast<uint4*>(to + 4 * k * row_bytes) = v;
+          if (4 * k < rows_on) *reinterpret_cast<uint4*>(to + 4 * k * row_bytes) = v;
         }
         __syncwarp();
       }
