@@ -227,6 +227,9 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     torch = _torch()
     if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # without a Stream object's microseconds
+        if raw is not None:
+            return int(raw(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream)
 
@@ -327,12 +330,24 @@ def csa_sparse_attn(args: AttnArgs, workspace=None, stream=None, device=None) ->
     _check(_attn(ctypes.byref(args), _ptr(workspace), nbytes, _stream(stream)), "csa_sparse_attn")
 
 
+def _on_device(args, stream, call, where: str) -> None:
+    """call(raw stream) on the device of the arguments' tensors, which need not
+    be the current one; ``stream`` None = that device's current stream."""
+    cuda = _torch().cuda
+    dev = getattr(args, "_device", None)
+    if dev is None or dev == cuda.current_device():
+        _check(call(_stream(stream)), where)
+        return
+    with cuda.device(dev):
+        _check(call(_stream(stream)), where)
+
+
 def csa_rms_norm(args: RmsNormArgs, stream=None) -> None:
-    _check(_rms_norm(ctypes.byref(args), _stream(stream)), "csa_rms_norm")
+    _on_device(args, stream, lambda st: _rms_norm(args, st), "csa_rms_norm")
 
 
 def csa_paged_append(args: PagedAppendArgs, stream=None) -> None:
-    _check(_paged_append(ctypes.byref(args), _stream(stream)), "csa_paged_append")
+    _on_device(args, stream, lambda st: _paged_append(args, st), "csa_paged_append")
 
 
 def csa_paged_attn_workspace_size(args: PagedAttnArgs) -> int:
@@ -342,9 +357,10 @@ def csa_paged_attn_workspace_size(args: PagedAttnArgs) -> int:
 def csa_paged_attn(args: PagedAttnArgs, workspace=None, stream=None, device=None) -> None:
     # the library checks a given workspace's size itself; query it only to allocate one
     if workspace is None:
-        workspace = _workspace(csa_paged_attn_workspace_size(args), device or "cuda")
+        dev = getattr(args, "_device", None)
+        workspace = _workspace(csa_paged_attn_workspace_size(args), device or ("cuda" if dev is None else f"cuda:{dev}"))
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_paged_attn(ctypes.byref(args), _ptr(workspace), nbytes, _stream(stream)), "csa_paged_attn")
+    _on_device(args, stream, lambda st: _paged_attn(args, _ptr(workspace), nbytes, st), "csa_paged_attn")
 
 
 def make_layer_array(layers: Sequence[LayerDesc]):
@@ -526,6 +542,14 @@ def _expect(t, dtype: str, what: str, shape=None, contiguous=False) -> None:
         raise ValueError(f"{what} must be contiguous")
 
 
+def _device_of(*tensors):
+    """Index of the CUDA device that all of the tensors are on (None: the CPU)."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
+    return devs.pop().index
+
+
 def _row_stride(t) -> int:
     """Stride of the first dimension; a single row's is arbitrary in torch."""
     if t.shape[0] > 1:
@@ -568,6 +592,7 @@ def rms_norm_args(*, x, out=None, residual=None, residual_out=None, weight=None,
         a.codes, a.codes_stride = _ptr(codes), _row_stride(codes)
     a.weight, a.eps = _ptr(weight), eps
     a._keep = (x, residual, residual_out, weight, out, codes, scales)
+    a._device = _device_of(*a._keep)
     return a
 
 
@@ -590,6 +615,7 @@ def paged_kv(*, pages, block_table, cu_q, kv_len) -> PagedKv:
     k.block_table, k.table_stride = _ptr(block_table), _row_stride(block_table)
     k.cu_q, k.kv_len = _ptr(cu_q), _ptr(kv_len)
     k._keep = (pages, block_table, cu_q, kv_len)
+    k._device = _device_of(*k._keep)
     return k
 
 
@@ -607,6 +633,7 @@ def paged_append_args(*, src, kv: PagedKv, norm: bool = False, weight=None, eps:
     a.src, a.n_rows, a.src_row_stride = _ptr(src), src.shape[0], _row_stride(src)
     a.norm, a.weight, a.eps, a.rope_cs = 1 if norm else 0, _ptr(weight), eps, _ptr(rope_cs)
     a._keep = (kv, src, weight, rope_cs)
+    a._device = _device_of(kv._keep[0], *a._keep[1:])
     return a
 
 
@@ -628,4 +655,5 @@ def paged_attn_args(*, q, kv: PagedKv, out, softmax_scale: float, lse=None, sink
     a.out, a.lse, a.softmax_scale, a.window = _ptr(out), _ptr(lse), softmax_scale, window
     a.sink, a.rope_cs = _ptr(sink), _ptr(rope_cs)
     a._keep = (kv, q, out, lse, sink, rope_cs)
+    a._device = _device_of(kv._keep[0], *a._keep[1:])
     return a

@@ -8,8 +8,10 @@
 // lanes of one warp, and their maxima meet by shuffles.
 //   dim <= 1024 : one warp per row (no shared memory, no barrier).
 //   else        : one CTA of dim / (8 C) threads per row.
-// CTAs stay for several rows, the norm's weight in registers: re-reading
-// 4 * dim bytes of it from L2 for every row would double the SM's loads.
+// CTAs stay for several rows and load the next one before they reduce this
+// one, so that loads are in flight through the barrier and the stores.
+#include <algorithm>
+
 #include "common.cuh"
 #include "encode.cuh"
 
@@ -64,7 +66,7 @@ CSA_DEV void store8(void* base, int64_t i, const float (&f)[8]) {
 
 // C chunks of 8 channels per thread; WARP_ROW: one warp per row, else one CTA.
 template <int SRC, int C, bool WARP_ROW>
-__global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rms_norm_kernel(NormParams p) {
+__global__ void __launch_bounds__(WARP_ROW ? 256 : 512) rms_norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int kV = SRC == CSA_SRC_F32 ? 2 : 1;   // 16-byte words per chunk
   constexpr int kEsz = SRC == CSA_SRC_F32 ? 4 : 2;
   __shared__ float part[2][32];
@@ -75,23 +77,8 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rms_norm_kernel(NormPar
   const int64_t row0 = WARP_ROW ? (int64_t)blockIdx.x * (blockDim.x >> 5) + warp : blockIdx.x;
   const int64_t step = WARP_ROW ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
   pdl_enter();
-  float w[C][8];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int ch = t + c * nt;
-    if (p.weight && ch < chunks) {
-      const float4 a = reinterpret_cast<const float4*>(p.weight)[2 * ch], b = reinterpret_cast<const float4*>(p.weight)[2 * ch + 1];
-      w[c][0] = a.x; w[c][1] = a.y; w[c][2] = a.z; w[c][3] = a.w;
-      w[c][4] = b.x; w[c][5] = b.y; w[c][6] = b.z; w[c][7] = b.w;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[c][k] = 1.f;
-    }
-  }
   const float inv_dim = 1.f / (float)p.dim;
-  int flip = 0;
-  for (int64_t r = row0; r < p.n_rows; r += step, flip ^= 1) {
-    uint4 xv[C][kV], rv[C][kV];
+  auto load_row = [&](int64_t r, uint4 (&xv)[C][kV], uint4 (&rv)[C][kV]) {
     const uint8_t* xr = static_cast<const uint8_t*>(p.x) + r * p.x_stride * kEsz;
     const uint8_t* rr = static_cast<const uint8_t*>(p.residual) + r * p.residual_stride * kEsz;
 #pragma unroll
@@ -103,6 +90,11 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rms_norm_kernel(NormPar
         if (p.residual) rv[c][v] = ch < chunks ? ld_stream_v4(rr + (int64_t)ch * 8 * kEsz + 16 * v) : make_uint4(0, 0, 0, 0);
       }
     }
+  };
+  int flip = 0;
+  uint4 xn[C][kV], rn[C][kV];
+  if (row0 < p.n_rows) load_row(row0, xn, rn);
+  for (int64_t r = row0; r < p.n_rows; r += step, flip ^= 1) {
     float s[C][8];
     float ss = 0.f;
 #pragma unroll
@@ -111,14 +103,14 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rms_norm_kernel(NormPar
       if (SRC == CSA_SRC_F32) {
 #pragma unroll
         for (int v = 0; v < kV; ++v) {
-          s[c][4 * v] = __uint_as_float(xv[c][v].x); s[c][4 * v + 1] = __uint_as_float(xv[c][v].y);
-          s[c][4 * v + 2] = __uint_as_float(xv[c][v].z); s[c][4 * v + 3] = __uint_as_float(xv[c][v].w);
-          f[4 * v] = __uint_as_float(rv[c][v].x); f[4 * v + 1] = __uint_as_float(rv[c][v].y);
-          f[4 * v + 2] = __uint_as_float(rv[c][v].z); f[4 * v + 3] = __uint_as_float(rv[c][v].w);
+          s[c][4 * v] = __uint_as_float(xn[c][v].x); s[c][4 * v + 1] = __uint_as_float(xn[c][v].y);
+          s[c][4 * v + 2] = __uint_as_float(xn[c][v].z); s[c][4 * v + 3] = __uint_as_float(xn[c][v].w);
+          f[4 * v] = __uint_as_float(rn[c][v].x); f[4 * v + 1] = __uint_as_float(rn[c][v].y);
+          f[4 * v + 2] = __uint_as_float(rn[c][v].z); f[4 * v + 3] = __uint_as_float(rn[c][v].w);
         }
       } else {
-        unpack_bf16x8(xv[c][0], s[c]);
-        unpack_bf16x8(rv[c][0], f);
+        unpack_bf16x8(xn[c][0], s[c]);
+        unpack_bf16x8(rn[c][0], f);
       }
       if (p.residual) {
 #pragma unroll
@@ -126,6 +118,11 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rms_norm_kernel(NormPar
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) ss = fmaf(s[c][k], s[c][k], ss);
+    }
+    // the next row is another one, so an output over its own inputs is safe
+    if (r + step < p.n_rows) load_row(r + step, xn, rn);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
       const int ch = t + c * nt;
       if (p.residual_out && ch < chunks) store8<SRC>(p.residual_out, r * p.residual_out_stride + 8 * ch, s[c]);
     }
@@ -142,10 +139,16 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 1024) rms_norm_kernel(NormPar
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int ch = t + c * nt;
+      float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+      if (p.weight && ch < chunks) {
+        const float4 a = reinterpret_cast<const float4*>(p.weight)[2 * ch], b = reinterpret_cast<const float4*>(p.weight)[2 * ch + 1];
+        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+      }
       float amax = 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        s[c][k] = s[c][k] * rs * w[c][k];
+        s[c][k] = s[c][k] * rs * w[k];
         amax = fmaxf(amax, fabsf(s[c][k]));
       }
       if (p.out && ch < chunks) store8<SRC>(p.out, r * p.out_stride + 8 * ch, s[c]);
@@ -194,11 +197,12 @@ static void launch_norm_src(const NormParams& p, cudaStream_t stream) {
     else launch_norm_t<SRC, 4, true>(p, 256, g, stream);
     return;
   }
-  const int threads = ((chunks + 1) / 2 + 31) / 32 * 32;   // dim <= 16384: at most 1024
-  int64_t per_sm = 1536 / threads;
-  if (per_sm < 1) per_sm = 1;
-  int64_t g = p.n_rows < kNumSMs * per_sm ? p.n_rows : kNumSMs * per_sm;
-  launch_norm_t<SRC, 2, false>(p, threads, g, stream);
+  const int C = chunks <= 1024 ? 2 : 4;                     // dim <= 16384: at most 512 threads
+  const int threads = ((chunks + C - 1) / C + 31) / 32 * 32;
+  const int64_t per_sm = std::max(1, (C == 2 && SRC == CSA_SRC_BF16 ? 1024 : 512) / threads);   // by registers
+  const int64_t g = std::min(p.n_rows, kNumSMs * per_sm);
+  if (C == 2) launch_norm_t<SRC, 2, false>(p, threads, g, stream);
+  else launch_norm_t<SRC, 4, false>(p, threads, g, stream);
 }
 
 cudaError_t launch_rms_norm(const csa_norm_args* a, cudaStream_t stream) {
