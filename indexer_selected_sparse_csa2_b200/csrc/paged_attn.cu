@@ -639,8 +639,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         ok = pg_wait_warp(q_full, seg++ & 1u, kErrWaitTmaFull);
         for (int i = 0; i < w.take && ok; ++i, ++t) {
           const uint32_t si = t & 1u;
-          ok = pg_wait_warp(k_full + t % kPgKBufs, (t / kPgKBufs) & 1u, kErrWaitTmaFull);
-          if (ok && t >= 2) ok = pg_wait_warp(s_free + si, ((t >> 1) - 1) & 1u, kErrWaitAccEmpty);
+          if (t >= 2) ok = pg_wait_warp(s_free + si, ((t >> 1) - 1) & 1u, kErrWaitAccEmpty);
+          ok = ok && pg_wait_warp(k_full + t % kPgKBufs, (t / kPgKBufs) & 1u, kErrWaitTmaFull);
           if (!ok) break;
           tc_fence_after();
           const uint32_t kd = kd0 + (t % kPgKBufs) * (kPgKBytes >> 4), sd = tbase + kPgSCol + 32 * si;
