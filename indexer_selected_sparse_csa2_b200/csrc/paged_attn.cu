@@ -345,14 +345,20 @@ CSA_DEV void pg_plan(const PgParams& p, const PgSmem& S, int pair, int pairs, in
   const csa_paged_attn_args& a = p.a;
   int64_t* gsum = reinterpret_cast<int64_t*>(S.v);
   const int groups = (a.kv.B + 31) / 32;
-  for (int g = warp; g < groups; g += kPgWarps) {
-    const int64_t u = pg_warp_sum64(pg_group_cost(p, g, lane));
-    if (lane == 0) gsum[g] = u;
+  if (groups > 1) {
+    for (int g = warp; g < groups; g += kPgWarps) {
+      const int64_t u = pg_warp_sum64(pg_group_cost(p, g, lane));
+      if (lane == 0) gsum[g] = u;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   if (warp == 0) {
-    int64_t total = 0;
-    for (int g = lane; g < groups; g += 32) total += gsum[g];
+    int64_t total = 0, only = 0;               // only: of the one group's sequences
+    if (groups > 1) {
+      for (int g = lane; g < groups; g += 32) total += gsum[g];
+    } else {
+      total = only = pg_group_cost(p, 0, lane);
+    }
     total = pg_warp_sum64(total);
     const int64_t G = min((int64_t)pairs, (total + 1) / 2);
     int64_t u0 = 0, u1 = 0;
@@ -364,7 +370,7 @@ CSA_DEV void pg_plan(const PgParams& p, const PgSmem& S, int pair, int pairs, in
     int b = 0, j = 0;
     if (u1 > u0) {
       int base = 0;
-      for (;; base += 32) {                                // the 32 groups
+      for (; groups > 1; base += 32) {                     // the 32 groups
         const int64_t v = base + lane < groups ? gsum[base + lane] : 0;
         const int64_t sum = pg_warp_sum64(v);
         if (at < sum || base + 32 >= groups) {
@@ -373,7 +379,7 @@ CSA_DEV void pg_plan(const PgParams& p, const PgSmem& S, int pair, int pairs, in
         }
         at -= sum;
       }
-      const int64_t v = pg_group_cost(p, base, lane);     // the sequence
+      const int64_t v = groups > 1 ? pg_group_cost(p, base, lane) : only;   // the sequence
       b = 32 * base + pg_locate(v, at, lane);
       const PgSeq s = pg_seq(a, b);
       for (;; j += 32) {                                   // the item
@@ -481,35 +487,36 @@ struct PgRowsOf {
 // come as they are, by asynchronous copies of whole rows (a row a lane would
 // touch 32 lines an instruction), into the group's K tile, which is free:
 // every S of the item before is done.  Rows past the item's are zero.
-// `wait` waits for that; after a failed wait (false) the warps only keep their
-// barriers.
+// pg_fetch_q issues the copies, pg_stage_q waits for them; after a failed wait
+// (`ok` false) the warps only keep their barriers.
 CSA_DEV void pg_cp_async16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
-template <typename Wait>
-CSA_DEV void pg_stage_q(const PgParams& p, const PgWalk& w, const PgRowsOf& R, const PgSmem& S, uint32_t tbase, int wl,
-                        int lane, int g, bool& ok, Wait wait) {
+CSA_DEV void pg_fetch_q(const PgParams& p, const PgWalk& w, const PgRowsOf& R, const PgSmem& S, int wl, int lane, int g) {
   const csa_paged_attn_args& a = p.a;
   const int r0 = w.j * kPgRows + R.base;
-  uint8_t* buf = S.k + g * kPgKBytes;                      // [64 rows][512 bytes], 16-byte chunk c of row r at c ^ (r & 31)
-  if (ok) ok = wait();
-  if (ok) {
-    const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + 256 * g + 8 * lane;
-    int head, tok = pg_div(r0 + 16 * wl, a.H, p.h_inv, head) + w.s.row0;
-    const uint32_t at = smem_u32(buf) + 16 * wl * 512;
+  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + 256 * g + 8 * lane;
+  int head, tok = pg_div(r0 + 16 * wl, a.H, p.h_inv, head) + w.s.row0;
+  // [64 rows][512 bytes], 16-byte chunk c of row r at c ^ (r & 31)
+  const uint32_t at = smem_u32(S.k + g * kPgKBytes) + 16 * wl * 512;
 #pragma unroll 4
-    for (int k = 0; k < 16; ++k) {                         // the warp's 16 rows
-      const bool on = 16 * wl + k < R.on;
-      pg_cp_async16(at + k * 512 + 16 * (lane ^ ((16 * wl + k) & 31)),
-                    on ? qb + (int64_t)tok * a.q_row_stride + (int64_t)head * a.q_head_stride : qb, on);
-      if (++head == a.H) {
-        head = 0;
-        ++tok;
-      }
+  for (int k = 0; k < 16; ++k) {                           // the warp's 16 rows
+    const bool on = 16 * wl + k < R.on;
+    pg_cp_async16(at + k * 512 + 16 * (lane ^ ((16 * wl + k) & 31)),
+                  on ? qb + (int64_t)tok * a.q_row_stride + (int64_t)head * a.q_head_stride : qb, on);
+    if (++head == a.H) {
+      head = 0;
+      ++tok;
     }
-    cp_async_commit();
-    cp_async_wait_all();
   }
+  cp_async_commit();
+}
+CSA_DEV void pg_stage_q(const PgParams& p, const PgWalk& w, const PgRowsOf& R, const PgSmem& S, uint32_t tbase, int wl,
+                        int lane, int g, bool ok) {
+  const csa_paged_attn_args& a = p.a;
+  const int r0 = w.j * kPgRows + R.base;
+  const uint8_t* buf = S.k + g * kPgKBytes;
+  cp_async_wait_all();
   named_bar(4 + g, 128);
   if (ok) {
     const int rr = (32 * wl + lane) & 63;
@@ -725,6 +732,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     // V.  (One CTA decoding for both, through distributed shared memory, spent
     // 3000 cycles a tile in the fence behind its remote stores.)
     const int wq = (warp - kPgWarpDec) & 3, g = (warp - kPgWarpDec) >> 2;
+    // the first item's query rows come first: their way is the longest
+    PgWalk w;
+    bool go = w.begin(p, S.start);
+    while (go && w.take == 0) go = w.next(p);
+    if (go) pg_fetch_q(p, w, PgRowsOf(a, w, rank), S, wq, lane, g);
     PgCursor cu;                       // the tile whose page table values are fetched next
     cu.begin(p, S.start, g);
     // page id and entry number in the page of entry 8 wq + (lane & 7), lanes
@@ -816,18 +828,19 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     auto st16 = [](uint32_t at, const uint4& q) {
       asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w) : "memory");
     };
-    PgWalk w;
     uint32_t t0 = 0, seg = 0;          // tiles before the item, items with tiles before it
     bool ok = true;
     // a failed wait leaves `ok` false and skips the later waits and all work;
     // every warp still passes its group's barriers once per item
-    for (bool go = w.begin(p, S.start); go; go = w.next(p)) {
+    for (; go; go = w.next(p)) {
       if (w.take == 0) continue;
-      pg_stage_q(p, w, PgRowsOf(a, w, rank), S, tbase, wq, lane, g, ok, [&]() {
-        const bool k = seg == 0 || pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty);
-        tc_fence_after();
-        return k;
-      });
+      const PgRowsOf R(a, w, rank);
+      if (seg > 0) {
+        ok = ok && pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty);
+        if (ok) pg_fetch_q(p, w, R, S, wq, lane, g);
+      }
+      tc_fence_after();
+      pg_stage_q(p, w, R, S, tbase, wq, lane, g, ok);
       if (ok && lane == 0) pg_arrive(q_full_at);
       ++seg;
       uint32_t t = t0 + ((t0 ^ (uint32_t)g) & 1u);
@@ -1186,48 +1199,57 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 // y, y + kPgCombRows, ... of the item that pair i of the attention began and
 // did not finish; its partials are slot 2i + 1 and then slot 2k of
 // k = i + 1, i + 2, ... up to the pair that ends the item, added in that order.
-constexpr int kPgCombRows = 32;
+// Latency counts here: the records of the next 32 pairs come with the first
+// one, and the first partials are loaded before their weights are known.
+constexpr int kPgCombRows = 64;
 __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PgParams p, int n_pairs) {
   pdl_enter();
   const csa_paged_attn_args& a = p.a;
   const int i = blockIdx.x, lane = threadIdx.x & 31;
   const PgMeta me = p.meta[i];
+  const PgMeta after = i + 1 + lane < n_pairs ? p.meta[i + 1 + lane] : PgMeta{0, 0, 0, 0, 0};
   if ((int)blockIdx.y >= me.rows) return;
-  int n = 1;                                   // partials
-  for (int k0 = i + 1; k0 < n_pairs; k0 += 32) {
-    const PgMeta mk = k0 + lane < n_pairs ? p.meta[k0 + lane] : PgMeta{0, 0, 0, 0, 0};
-    const uint32_t end = __ballot_sync(0xffffffffu, mk.cont && mk.done);
-    if (end) {
-      n = k0 - i + __ffs(end);
-      break;
-    }
-    n = min(k0 + 32, n_pairs) - i;
+  uint32_t end = __ballot_sync(0xffffffffu, after.cont && after.done);
+  int n = __ffs(end) + 1;                      // partials
+  for (int k0 = i + 33; !end; k0 += 32) {
+    const PgMeta mk = k0 + lane < n_pairs ? p.meta[k0 + lane] : PgMeta{0, 0, 0, 1, 1};
+    end = __ballot_sync(0xffffffffu, mk.cont && mk.done);
+    n = min(k0 - i + __ffs(end), n_pairs - i);
   }
   auto slot = [&](int s) { return (int64_t)(s == 0 ? 2 * i + 1 : 2 * (i + s)); };
   for (int row = blockIdx.y; row < me.rows; row += kPgCombRows) {
     const int64_t orow = me.row0 + row;
+    const float* po = p.part_o + (int64_t)row * kD + 4 * threadIdx.x;
+    constexpr int kR = 8;
+    float4 v[kR];
+#pragma unroll
+    for (int s = 0; s < kR; ++s)
+      v[s] = s < n ? *reinterpret_cast<const float4*>(po + slot(s) * (kPgRows * kD)) : make_float4(0.f, 0.f, 0.f, 0.f);
     const int head = (int)(orow % a.H);
     const float s0 = a.sink ? a.sink[head] * kPgLog2e : -INFINITY;
-    float M = -INFINITY;
-    for (int s = lane; s < n; s += 32) M = fmaxf(M, p.part_ml[slot(s) * kPgRows + row].x);
+    const float2 ml0 = lane < n ? p.part_ml[slot(lane) * kPgRows + row] : make_float2(-INFINITY, 0.f);
+    float M = ml0.x;
+    for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, p.part_ml[slot(s) * kPgRows + row].x);
     M = warp_max(M);
     M = fmaxf(M - kPgPExp, s0);
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* po = p.part_o + (int64_t)row * kD + 4 * threadIdx.x;
     for (int sb = 0; sb < n; sb += 32) {
-      float wt = 0.f;
-      if (sb + lane < n) {
-        const float2 ml = p.part_ml[slot(sb + lane) * kPgRows + row];
-        wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - kPgPExp - M);
-        L += wt * ml.y;
-      }
-      const int m = min(32, n - sb);
-#pragma unroll 8
-      for (int s = 0; s < m; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, wt, s);
-        const float4 v = *reinterpret_cast<const float4*>(po + slot(sb + s) * (kPgRows * kD));
-        acc.x += ws * v.x; acc.y += ws * v.y; acc.z += ws * v.z; acc.w += ws * v.w;
+      const float2 ml = sb == 0 ? ml0 : sb + lane < n ? p.part_ml[slot(sb + lane) * kPgRows + row] : make_float2(-INFINITY, 0.f);
+      const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - kPgPExp - M);
+      L += wt * ml.y;
+      for (int q = 0; q < 32 && sb + q < n; q += kR) {
+        if (sb + q > 0) {
+#pragma unroll
+          for (int s = 0; s < kR; ++s)
+            v[s] = sb + q + s < n ? *reinterpret_cast<const float4*>(po + slot(sb + q + s) * (kPgRows * kD)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int s = 0; s < kR; ++s) {
+          // a partial of weight 0 holds nothing (zeros past the last one)
+          const float ws = __shfl_sync(0xffffffffu, wt, q + s);
+          acc.x += ws * v[s].x; acc.y += ws * v[s].y; acc.z += ws * v[s].z; acc.w += ws * v[s].w;
+        }
       }
     }
     L = warp_sum(L);
