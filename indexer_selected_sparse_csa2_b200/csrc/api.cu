@@ -46,6 +46,7 @@ cudaError_t launch_paged_append(const csa_paged_append_args* a, cudaStream_t str
 size_t paged_attn_ws_bytes(const csa_paged_attn_args* a);
 cudaError_t launch_paged_attn(const csa_paged_attn_args* a, void* ws, cudaStream_t stream);
 int read_pg_error(bool clear);
+int read_p1_error(bool clear);
 
 static bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 static bool al16i(int64_t v) { return (v & 15) == 0; }
@@ -732,8 +733,8 @@ const char* csa_status_string(int32_t s) {
 
 int32_t csa_device_status(void) {
   const int a = read_tc_error(true), b = read_pf_error(true), c = read_at_error(true);
-  const int d = read_pk_error(true), e = read_mx_error(true), f = read_pg_error(true);
-  return (int32_t)(a ? a : (b ? b : (c ? c : (d ? d : (e ? e : f)))));
+  const int d = read_pk_error(true), e = read_mx_error(true), f = read_pg_error(true), g = read_p1_error(true);
+  return (int32_t)(a ? a : (b ? b : (c ? c : (d ? d : (e ? e : (f ? f : g))))));
 }
 
 uint64_t csa_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

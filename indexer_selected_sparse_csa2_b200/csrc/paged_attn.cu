@@ -43,65 +43,21 @@
 // CTA 0 for both).  In flight: two K tiles, four V tiles, two S and two P.  A
 // second softmax warpgroup left 96 registers a thread, and with shared memory
 // at its maximum a spilled register is a trip to L2.
-#include <climits>
-
-#include "sm100.cuh"
-#include "paged.cuh"
-#include "rope.cuh"
+#include "paged_attn.cuh"
 
 namespace csa {
 
 constexpr int kPgRows = 128;              // query rows per item (two CTAs)
 constexpr int kPgHalf = 64;               // ... per CTA
-constexpr int kPgE = 64;                  // entries per key tile
-constexpr int kPgOwn = 32;                // ... decoded by one CTA
 constexpr int kPgKBufs = 2, kPgVBufs = 3; // K and V tiles in flight
-constexpr int kPgWarpDec = 4;             // first decode warp (two groups of 4)
-constexpr int kPgWarpS = 12;
-constexpr int kPgWarpPV = 13;
-constexpr int kPgWarps = 14;
-constexpr int kPgThreads = 32 * kPgWarps;
-constexpr int kPgQTmemBlocks = 6;         // 64-channel blocks of Q in TMEM
 constexpr int kPgQBlk = kPgHalf * 128;    // shared Q block: 64 rows x 64 fp16
-constexpr int kPgKBlk = kPgOwn * 128;     // 64-channel block of a K tile
-constexpr int kPgKBytes = 8 * kPgKBlk;
 constexpr int kPgVBlk = kPgE * 128;       // 64-channel block of a V tile
 constexpr int kPgVBytes = 4 * kPgVBlk;
 constexpr int kPgPBytes = kPgHalf * kPgE * 2;
-constexpr uint32_t kPgSCol = 32 * kPgQTmemBlocks;   // two S tiles of 32 columns
-constexpr uint32_t kPgOCol = 256;
-constexpr uint32_t kPgTmemCols = 512;
-static_assert(kPgSCol + kPgE <= kPgOCol, "TMEM map");
-constexpr int kPgItemCost = 4;            // an item's own cost (Q, output) in key tiles
-constexpr float kPgRescale = 8.0f;        // lazy-rescale threshold (exp2 units)
-constexpr float kPgPExp = 6.0f;           // P carries a factor 2^6
-constexpr float kPgLog2e = 1.4426950408889634f;
-constexpr float kPgLn2 = 0.6931471805599453f;
-constexpr int kPgMaxB = 65536;
 constexpr size_t kPgOperandBytes = 2 * kPgQBlk + kPgKBufs * kPgKBytes + kPgVBufs * kPgVBytes + 2 * kPgPBytes;
 constexpr size_t kPgSmemBytes = kPgOperandBytes + 3072;
 static_assert(kPgSmemBytes <= 232448, "shared memory of a CTA");
 static_assert(kPgMaxB / 32 * 8 <= kPgVBufs * kPgVBytes, "the plan's group sums use the V tiles");
-
-static __device__ int g_pg_error;
-
-// What a pair of CTAs left for the combine.
-struct PgMeta {
-  int64_t row0;      // leader: first output row (token * H + head) of its last item
-  int32_t rows;      // leader: rows of that item; 0 = its last item is not split here
-  int32_t cont;      // its first item began in an earlier pair ...
-  int32_t done;      // ... and ends here
-  int32_t pad;
-};
-
-struct PgParams {
-  csa_paged_attn_args a;
-  float scale_log2;  // softmax_scale * log2(e)
-  uint32_t page_inv, h_inv;   // pg_inv of page_size and H
-  float* part_o;     // [2 * pairs][128][512] fp32
-  float2* part_ml;   // [2 * pairs][128] (max, sum)
-  PgMeta* meta;      // [pairs]
-};
 
 struct PgSmem {
   uint8_t* q;        // channels 384..511 of Q: 2 blocks
@@ -131,19 +87,7 @@ CSA_DEV PgSmem carve_pg(uint8_t* p) {
   return s;
 }
 
-CSA_DEV uint32_t pg_h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-CSA_DEV __half2 pg_u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-CSA_DEV float pg_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // ------------------------------------------------- barriers across the pair --
-// Bounded wait by a whole warp, the same answer in every lane.
-CSA_DEV bool pg_wait_warp(uint64_t* bar, uint32_t parity, int code) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_pg_error, code));
-}
 // Arrival on CTA 0's barrier (`bar` is its address in the cluster's window).
 // What it publishes lies in the arriving CTA's own shared memory or TMEM,
 // where the pair's MMAs read it on the same SM.
@@ -156,13 +100,6 @@ CSA_DEV void pg_commit(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
       ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
-// MMAs with descriptors given by their low words (the high word is a constant
-// of the layout: 128-byte swizzle, 8-row groups 1024 bytes apart), so that an
-// unrolled sequence costs one addition per operand; issued by one lane of a
-// warp that runs its loops as a whole.
-constexpr uint32_t kPgDesc = (1024u >> 4) | 1u << 14 | 2u << 29;
-CSA_DEV uint32_t pg_desc_k(uint32_t smem_addr) { return (smem_addr >> 4) | 1u << 16; }
-CSA_DEV uint32_t pg_desc_mn(uint32_t smem_addr, uint32_t lbo) { return (smem_addr >> 4) | (lbo >> 4) << 16; }
 template <bool ACC>
 CSA_DEV void pg_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
   asm volatile(
@@ -181,403 +118,19 @@ CSA_DEV void pg_st32(void* p, const uint32_t* v) {   // 32 bytes, aligned
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
                "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
 }
-CSA_DEV bool pg_elect() {
-  uint32_t e;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
-  return e != 0;
-}
 // Instruction descriptor with B MN-major (bit 16).
 constexpr uint32_t kPgIdescS = (1u << 4) | ((uint32_t)(kPgE >> 3) << 17) | ((uint32_t)(kPgRows >> 4) << 24);
 constexpr uint32_t kPgIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(kPgRows >> 4) << 24);
-
-// n / d for 0 <= n < 2^31: the product with floor(2^32 / d) is at most one short
-// (d = 1: with 2^32 - 1).
-static uint32_t pg_inv(uint32_t d) { return d == 1 ? 0xffffffffu : (uint32_t)(((uint64_t)1 << 32) / d); }
-CSA_DEV int pg_div(int n, int d, uint32_t inv, int& rem) {
-  uint32_t q = __umulhi((uint32_t)n, inv), r = (uint32_t)n - q * (uint32_t)d;
-  if (r >= (uint32_t)d) {
-    ++q;
-    r -= (uint32_t)d;
-  }
-  rem = (int)r;
-  return (int)q;
-}
-CSA_DEV int pg_div(int n, int d, uint32_t inv) {
-  int r;
-  return pg_div(n, d, inv, r);
-}
-
-// ------------------------------------------------------------- work items --
-struct PgSeq {
-  int n;        // new tokens
-  int kv;       // cache length with them, >= 0
-  int row0;     // first packed row
-  int tiles;    // items of 128 (token, head) rows
-};
-CSA_DEV PgSeq pg_seq(const csa_paged_attn_args& a, int b) {
-  PgSeq s;
-  const int hi = (int)a.n_rows;
-  s.row0 = min(max(a.kv.cu_q[b], 0), hi);
-  s.n = min(max(a.kv.cu_q[b + 1], s.row0), hi) - s.row0;
-  s.kv = max(a.kv.kv_len[b], 0);
-  s.tiles = (int)(((int64_t)s.n * a.H + kPgRows - 1) / kPgRows);
-  return s;
-}
-// Positions [k0, k1) that the rows of item j see (k1 = k0: none), before the
-// rows' own masks.  Row r of the item is (token, head) row 128 j + r.
-CSA_DEV void pg_item(const PgParams& p, const PgSeq& s, int j, int& k0, int& k1) {
-  const csa_paged_attn_args& a = p.a;
-  const int r0 = j * kPgRows, r1 = min(r0 + kPgRows, s.n * a.H) - 1;
-  const int p0 = s.kv - s.n + pg_div(r0, a.H, p.h_inv), p1 = s.kv - s.n + pg_div(r1, a.H, p.h_inv);
-  k1 = min(p1 + 1, a.kv.max_pages * a.kv.page_size);
-  k0 = a.window ? max(0, p0 + 1 > a.window ? p0 + 1 - a.window : 0) : 0;
-  if (k1 < k0) k1 = k0;
-}
-CSA_DEV int pg_tiles(int k0, int k1) { return (k1 - k0 + kPgE - 1) / kPgE; }
-
-// A pair's walk over its items.  An item of T key tiles spans kPgItemCost + T
-// of the cost axis; the pair takes the tiles whose place lies in its range.
-struct PgWalk {
-  int64_t left;    // cost left, from this item's start in the range on
-  int b, j;        // sequence, item
-  int at;          // where in the item the range starts
-  PgSeq s;
-  int k0, k1, total;   // the item's positions and key tiles
-  int off, take;       // first key tile taken here, number taken
-  CSA_DEV void item(const PgParams& p) {
-    pg_item(p, s, j, k0, k1);
-    total = pg_tiles(k0, k1);
-    off = min(max(at - kPgItemCost, 0), total);
-    take = (int)min((int64_t)total, max(at + left - kPgItemCost, (int64_t)0)) - off;
-  }
-  // does this pair do anything for the item? (a tileless one belongs to the
-  // pair at its start)
-  CSA_DEV bool mine() const { return take > 0 || (total == 0 && at == 0); }
-  CSA_DEV void settle(const PgParams& p) {
-    while (left > 0 && !mine()) step(p);
-  }
-  CSA_DEV void step(const PgParams& p) {
-    left -= kPgItemCost + total - at;
-    at = 0;
-    if (left <= 0) return;
-    if (++j >= s.tiles) {
-      j = 0;
-      do {
-        if (++b >= p.a.kv.B) { left = 0; return; }
-        s = pg_seq(p.a, b);
-      } while (s.tiles == 0);
-    }
-    item(p);
-  }
-  CSA_DEV bool begin(const PgParams& p, const int64_t* start) {
-    at = (int)start[0];
-    left = start[1];
-    b = (int)start[2];
-    j = (int)start[3];
-    if (left <= 0) return false;
-    s = pg_seq(p.a, b);
-    item(p);
-    settle(p);
-    return left > 0;
-  }
-  CSA_DEV bool next(const PgParams& p) {
-    step(p);
-    settle(p);
-    return left > 0;
-  }
-};
-
-CSA_DEV int64_t pg_warp_sum64(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-// Cost of sequences 32 g + lane (0 past the last).  Sequences with many
-// items are summed by the whole warp.
-CSA_DEV int64_t pg_group_cost(const PgParams& p, int g, int lane) {
-  const csa_paged_attn_args& a = p.a;
-  const int b = 32 * g + lane;
-  PgSeq s{0, 0, 0, 0};
-  if (b < a.kv.B) s = pg_seq(a, b);
-  int64_t u = 0;
-  if (s.tiles <= 4) {
-    for (int j = 0; j < s.tiles; ++j) {
-      int k0, k1;
-      pg_item(p, s, j, k0, k1);
-      u += kPgItemCost + pg_tiles(k0, k1);
-    }
-  }
-  for (uint32_t big = __ballot_sync(0xffffffffu, s.tiles > 4); big; big &= big - 1) {
-    const int l = __ffs(big) - 1;
-    PgSeq q;
-    q.n = __shfl_sync(0xffffffffu, s.n, l);
-    q.kv = __shfl_sync(0xffffffffu, s.kv, l);
-    q.row0 = 0;
-    q.tiles = __shfl_sync(0xffffffffu, s.tiles, l);
-    int64_t v = 0;
-    for (int j = lane; j < q.tiles; j += 32) {
-      int k0, k1;
-      pg_item(p, q, j, k0, k1);
-      v += kPgItemCost + pg_tiles(k0, k1);
-    }
-    v = pg_warp_sum64(v);
-    if (lane == l) u = v;
-  }
-  return u;
-}
-// Lane whose value the running sum `at` (0 <= at < the warp's sum) falls in;
-// `at` becomes the offset inside it.  v >= 0.
-CSA_DEV int pg_locate(int64_t v, int64_t& at, int lane) {
-  int64_t inc = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += u;
-  }
-  const int l = __ffs(__ballot_sync(0xffffffffu, at < inc)) - 1;
-  const int64_t before = __shfl_sync(0xffffffffu, inc - v, l < 0 ? 0 : l);
-  at -= before;
-  return l < 0 ? 0 : l;
-}
-// Finds the range of the cost axis of pair `pair` of `pairs`; every warp of a
-// CTA takes part, both CTAs find the same.
-CSA_DEV void pg_plan(const PgParams& p, const PgSmem& S, int pair, int pairs, int warp, int lane) {
-  const csa_paged_attn_args& a = p.a;
-  int64_t* gsum = reinterpret_cast<int64_t*>(S.v);
-  const int groups = (a.kv.B + 31) / 32;
-  if (groups > 1) {
-    for (int g = warp; g < groups; g += kPgWarps) {
-      const int64_t u = pg_warp_sum64(pg_group_cost(p, g, lane));
-      if (lane == 0) gsum[g] = u;
-    }
-    __syncthreads();
-  }
-  if (warp == 0) {
-    int64_t total = 0, only = 0;               // only: of the one group's sequences
-    if (groups > 1) {
-      for (int g = lane; g < groups; g += 32) total += gsum[g];
-    } else {
-      total = only = pg_group_cost(p, 0, lane);
-    }
-    total = pg_warp_sum64(total);
-    const int64_t G = min((int64_t)pairs, (total + 1) / 2);
-    int64_t u0 = 0, u1 = 0;
-    if (pair < G) {
-      u0 = total * pair / G;
-      u1 = total * (pair + 1) / G;
-    }
-    int64_t at = u0;
-    int b = 0, j = 0;
-    if (u1 > u0) {
-      int base = 0;
-      for (; groups > 1; base += 32) {                     // the 32 groups
-        const int64_t v = base + lane < groups ? gsum[base + lane] : 0;
-        const int64_t sum = pg_warp_sum64(v);
-        if (at < sum || base + 32 >= groups) {
-          base += pg_locate(v, at, lane);
-          break;
-        }
-        at -= sum;
-      }
-      const int64_t v = groups > 1 ? pg_group_cost(p, base, lane) : only;   // the sequence
-      b = 32 * base + pg_locate(v, at, lane);
-      const PgSeq s = pg_seq(a, b);
-      for (;; j += 32) {                                   // the item
-        int64_t w = 0;
-        if (j + lane < s.tiles) {
-          int k0, k1;
-          pg_item(p, s, j + lane, k0, k1);
-          w = kPgItemCost + pg_tiles(k0, k1);
-        }
-        const int64_t sum = pg_warp_sum64(w);
-        if (at < sum || j + 32 >= s.tiles) {
-          j += pg_locate(w, at, lane);
-          break;
-        }
-        at -= sum;
-      }
-    }
-    if (lane == 0) {
-      S.start[0] = at;
-      S.start[1] = u1 - u0;
-      S.start[2] = b;
-      S.start[3] = j;
-    }
-  }
-  __syncthreads();
-}
-
-// --------------------------------------------------------------- decoding --
-CSA_DEV void pg_bf16x8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[2 * k] = __uint_as_float(w[k] << 16);
-    f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-  }
-}
-CSA_DEV uint4 pg_f16x8(const float (&f)[8]) {
-  return make_uint4(pg_h2u(__floats2half2_rn(f[0], f[1])), pg_h2u(__floats2half2_rn(f[2], f[3])),
-                    pg_h2u(__floats2half2_rn(f[4], f[5])), pg_h2u(__floats2half2_rn(f[6], f[7])));
-}
-// The conversion instructions run at the rate of the ALU here (2 cycles a warp
-// and scheduler, as LOP3 or HMUL2), so they beat decoding by shifts and masks
-// (two of them and a shift against seven for 4 FP8 codes).
-// 8 FP8 codes times f (a power of two, twice).
-CSA_DEV uint4 pg_decode_fp8(uint32_t w0, uint32_t w1, __half2 f) {
-  return make_uint4(pg_h2u(__hmul2(dec_e4m3x2(w0), f)), pg_h2u(__hmul2(dec_e4m3x2(w0 >> 16), f)),
-                    pg_h2u(__hmul2(dec_e4m3x2(w1), f)), pg_h2u(__hmul2(dec_e4m3x2(w1 >> 16), f)));
-}
-// 2^(byte - 127) twice in fp16 (0 for byte 0, whose block decodes to less than
-// half of fp16's smallest value).
-CSA_DEV __half2 pg_fp8_scale(uint32_t byte) {
-  const float f = __uint_as_float(byte << 23);
-  return __floats2half2_rn(f, f);
-}
-// Exponent bytes that pg_fp8_scale does not hold exactly: 1..102 and 143..255.
-CSA_DEV bool pg_fp8_far(uint32_t bytes) {
-  return (__vcmpgtu4(__vsub4(bytes, 0x67676767u), 0x27272727u) & ~__vcmpeq4(bytes, 0u)) != 0u;
-}
-// ... for those: fp32 products, rounded to fp16.
-CSA_DEV uint4 pg_decode_fp8_far(uint32_t w0, uint32_t w1, uint32_t byte) {
-  const float s = exp2f((float)((int)byte - 127));
-  const float2 a = __half22float2(dec_e4m3x2(w0)), b = __half22float2(dec_e4m3x2(w0 >> 16));
-  const float2 c = __half22float2(dec_e4m3x2(w1)), d = __half22float2(dec_e4m3x2(w1 >> 16));
-  const float f[8] = {a.x * s, a.y * s, b.x * s, b.y * s, c.x * s, c.y * s, d.x * s, d.y * s};
-  return pg_f16x8(f);
-}
-// One word of 8 FP4 codes times the block scale s (twice): at most 6
-// significant bits between 2^-10 and 2688, exact in fp16.
-CSA_DEV uint4 pg_decode_fp4(uint32_t w, __half2 s) {
-  return make_uint4(pg_h2u(__hmul2(dec_e2m1x2(w & 0xFF), s)), pg_h2u(__hmul2(dec_e2m1x2((w >> 8) & 0xFF), s)),
-                    pg_h2u(__hmul2(dec_e2m1x2((w >> 16) & 0xFF), s)), pg_h2u(__hmul2(dec_e2m1x2(w >> 24), s)));
-}
-// w[m] becomes w[m ^ q] (q in 0..3).
-CSA_DEV void pg_rotate(uint4& v, int q) {
-  if (q & 1) v = make_uint4(v.y, v.x, v.w, v.z);
-  if (q & 2) v = make_uint4(v.z, v.w, v.x, v.y);
-}
-// 32 FP4 codes and the block scales of their halves (E4M3 codes in bytes 0 and
-// 1 of `two`) as four 8-channel chunks, chunk m ^ q at place m.
-CSA_DEV void pg_decode_fp4x32(uint4 v, uint32_t two, int q, uint4 (&c)[4]) {
-  const __half2 s = dec_e4m3x2((q & 2) ? __byte_perm(two, 0, 0x4401) : two);
-  const __half2 sa = __low2half2(s), sb = __high2half2(s);
-  pg_rotate(v, q);
-  c[0] = pg_decode_fp4(v.x, sa);
-  c[1] = pg_decode_fp4(v.y, sa);
-  c[2] = pg_decode_fp4(v.z, sb);
-  c[3] = pg_decode_fp4(v.w, sb);
-}
 
 // The rows of an item that CTA `rank` works on: its `per` rows from rank * per
 // on, `per` a half of the item's rows rounded up, so a short item's output is
 // shared out too.
 struct PgRowsOf {
   int base, on;      // first row in the item, rows
-  CSA_DEV PgRowsOf(const csa_paged_attn_args& a, const PgWalk& w, uint32_t rank) {
+  CSA_DEV PgRowsOf(const csa_paged_attn_args& a, const PgWalk<kPgRows>& w, uint32_t rank) {
     const int n = min(w.s.n * a.H - w.j * kPgRows, kPgRows), per = (n + 1) >> 1;
     base = (int)rank * per;
     on = min(per, n - base);
-  }
-};
-
-// Stages channels 256 g .. of this CTA's query rows of an item, by the 4 warps
-// of decode group g: channels below 384 into TMEM (twice: lanes L and L + 64
-// hold row L), the last 128 into the shared blocks, all as fp16.  The rows
-// come as they are, by asynchronous copies of whole rows (a row a lane would
-// touch 32 lines an instruction), into the group's K tile, which is free:
-// every S of the item before is done.  Rows past the item's are zero.
-// pg_fetch_q issues the copies, pg_stage_q waits for them; after a failed wait
-// (`ok` false) the warps only keep their barriers.
-CSA_DEV void pg_cp_async16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
-}
-CSA_DEV void pg_fetch_q(const PgParams& p, const PgWalk& w, const PgRowsOf& R, const PgSmem& S, int wl, int lane, int g) {
-  const csa_paged_attn_args& a = p.a;
-  const int r0 = w.j * kPgRows + R.base;
-  const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + 256 * g + 8 * lane;
-  int head, tok = pg_div(r0 + 16 * wl, a.H, p.h_inv, head) + w.s.row0;
-  // [64 rows][512 bytes], 16-byte chunk c of row r at c ^ (r & 31)
-  const uint32_t at = smem_u32(S.k + g * kPgKBytes) + 16 * wl * 512;
-#pragma unroll 4
-  for (int k = 0; k < 16; ++k) {                           // the warp's 16 rows
-    const bool on = 16 * wl + k < R.on;
-    pg_cp_async16(at + k * 512 + 16 * (lane ^ ((16 * wl + k) & 31)),
-                  on ? qb + (int64_t)tok * a.q_row_stride + (int64_t)head * a.q_head_stride : qb, on);
-    if (++head == a.H) {
-      head = 0;
-      ++tok;
-    }
-  }
-  cp_async_commit();
-}
-CSA_DEV void pg_stage_q(const PgParams& p, const PgWalk& w, const PgRowsOf& R, const PgSmem& S, uint32_t tbase, int wl,
-                        int lane, int g, bool ok) {
-  const csa_paged_attn_args& a = p.a;
-  const int r0 = w.j * kPgRows + R.base;
-  const uint8_t* buf = S.k + g * kPgKBytes;
-  cp_async_wait_all();
-  named_bar(4 + g, 128);
-  if (ok) {
-    const int rr = (32 * wl + lane) & 63;
-    const uint8_t* from = buf + rr * 512;
-#pragma unroll 2
-    for (int c = 0; c < (g ? 16 : 32); c += 4) {           // 16 columns
-      uint32_t o[16];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float f[8];
-        pg_bf16x8(*reinterpret_cast<const uint4*>(from + 16 * ((c + k) ^ (rr & 31))), f);
-        const uint4 h = pg_f16x8(f);
-        o[4 * k] = h.x;
-        o[4 * k + 1] = h.y;
-        o[4 * k + 2] = h.z;
-        o[4 * k + 3] = h.w;
-      }
-      tmem_st16(tbase + ((uint32_t)(32 * wl) << 16) + 128u * g + 4u * c, o);
-    }
-    if (g == 1) {
-#pragma unroll 2
-      for (int k = 0; k < 8; ++k) {                        // 8 rows x 16 chunks of the last 128 channels
-        const int r = 8 * k + 2 * wl + (lane >> 4), c = lane & 15;
-        float f[8];
-        pg_bf16x8(*reinterpret_cast<const uint4*>(buf + r * 512 + 16 * ((16 + c) ^ (r & 31))), f);
-        if (a.rope_cs && c >= 8 && r < R.on) {             // channels 448 + 8 (c - 8) ..
-          const int tok = w.s.row0 + pg_div(r0 + r, a.H, p.h_inv);
-          const float4* cs = reinterpret_cast<const float4*>(a.rope_cs + (int64_t)tok * 64 + 8 * (c - 8));
-          const float4 ca = cs[0], cb = cs[1];
-          float2 x;
-          x = rope_fwd(f[0], f[1], ca.x, ca.y); f[0] = x.x; f[1] = x.y;
-          x = rope_fwd(f[2], f[3], ca.z, ca.w); f[2] = x.x; f[3] = x.y;
-          x = rope_fwd(f[4], f[5], cb.x, cb.y); f[4] = x.x; f[5] = x.y;
-          x = rope_fwd(f[6], f[7], cb.z, cb.w); f[6] = x.x; f[7] = x.y;
-        }
-        *reinterpret_cast<uint4*>(S.q + (c >> 3) * kPgQBlk + sw128_offset_h(r, 8 * (c & 7))) = pg_f16x8(f);
-      }
-    }
-    tmem_wait_st();
-    fence_proxy_async_smem();
-    tc_fence_before();
-  }
-  named_bar(4 + g, 128);                                   // the K tile is read
-}
-
-// A position in the pair's list of key tiles.
-struct PgCursor {
-  PgWalk w;
-  int i;           // tile of the item
-  bool live;
-  CSA_DEV void begin(const PgParams& p, const int64_t* start, int skip) {
-    live = w.begin(p, start);
-    i = 0;
-    advance(p, skip);
-  }
-  CSA_DEV void advance(const PgParams& p, int n) {
-    i += n;
-    while (live && i >= w.take) {
-      i -= w.take;
-      live = w.next(p);
-    }
   }
 };
 
@@ -628,7 +181,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   pdl_wait();
-  pg_plan(p, S, pair, pairs, warp, lane);
+  pg_plan<kPgRows>(p, reinterpret_cast<int64_t*>(S.v), S.start, pair, pairs, warp, kPgWarps, lane);
   tc_fence_before();
   cluster_sync_all();                // barriers and TMEM of both CTAs are there
   tc_fence_after();
@@ -638,7 +191,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     // ------------------------------------------------------------ S issuer
     if (rank == 0) {
       const uint32_t qd = pg_desc_k(smem_u32(S.q)), kd0 = pg_desc_k(smem_u32(S.k));
-      PgWalk w;
+      PgWalk<kPgRows> w;
       uint32_t t = 0, seg = 0;
       bool ok = true;
       for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
@@ -674,7 +227,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     // ----------------------------------------------------------- PV issuer
     if (rank == 0) {
       const uint32_t vd0 = pg_desc_mn(smem_u32(S.v), kPgVBlk), pd0 = pg_desc_k(smem_u32(S.p));
-      PgWalk w;
+      PgWalk<kPgRows> w;
       uint32_t t = 0;
       bool ok = true;
       for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
@@ -705,7 +258,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     } else {
       // CTA 1's warp fetches the next item's query rows, of both CTAs, into L2
       // once an item's last S is done
-      PgWalk w;
+      PgWalk<kPgRows> w;
       uint32_t seg = 0;
       bool ok = true;
       for (bool go = w.begin(p, S.start); go && ok;) {
@@ -733,11 +286,16 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     // 3000 cycles a tile in the fence behind its remote stores.)
     const int wq = (warp - kPgWarpDec) & 3, g = (warp - kPgWarpDec) >> 2;
     // the first item's query rows come first: their way is the longest
-    PgWalk w;
+    PgWalk<kPgRows> w;
     bool go = w.begin(p, S.start);
     while (go && w.take == 0) go = w.next(p);
-    if (go) pg_fetch_q(p, w, PgRowsOf(a, w, rank), S, wq, lane, g);
-    PgCursor cu;                       // the tile whose page table values are fetched next
+    auto rows = [&]() {
+      const PgRowsOf R(a, w, rank);
+      return PgRowsIn{w.s.row0, w.j * kPgRows + R.base, R.on};
+    };
+    uint8_t* q_buf = S.k + g * kPgKBytes;                  // free between an item's last S and the next one's first tile
+    if (go) pg_fetch_q(p, rows(), q_buf, wq, lane, g);
+    PgCursor<kPgRows> cu;                       // the tile whose page table values are fetched next
     cu.begin(p, S.start, g);
     // page id and entry number in the page of entry 8 wq + (lane & 7), lanes
     // 8-15 (24-31) of the other CTA's half, of the tile whose entries are
@@ -834,13 +392,13 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     // every warp still passes its group's barriers once per item
     for (; go; go = w.next(p)) {
       if (w.take == 0) continue;
-      const PgRowsOf R(a, w, rank);
+      const PgRowsIn R = rows();
       if (seg > 0) {
         ok = ok && pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty);
-        if (ok) pg_fetch_q(p, w, R, S, wq, lane, g);
+        if (ok) pg_fetch_q(p, R, q_buf, wq, lane, g);
       }
       tc_fence_after();
-      pg_stage_q(p, w, R, S, tbase, wq, lane, g, ok);
+      pg_stage_q<false>(p, R, q_buf, S.q, tbase, wq, lane, g, ok);
       if (ok && lane == 0) pg_arrive(q_full_at);
       ++seg;
       uint32_t t = t0 + ((t0 ^ (uint32_t)g) & 1u);
@@ -959,7 +517,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     const bool zero = p.scale_log2 == 0.f;
     const float sc = zero ? 1.f : p.scale_log2;
     const uint32_t s_free_at = dsmem(s_free, 0), p_full_at = dsmem(p_full, 0);
-    PgWalk w;
+    PgWalk<kPgRows> w;
     uint32_t t = 0, seg = 0;
     bool ok = true;
     int64_t meta_row0 = 0;
@@ -1195,26 +753,26 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
   }
 }
 
-// Joins the partials of the items that several pairs share.  CTA (i, y): rows
-// y, y + kPgCombRows, ... of the item that pair i of the attention began and
-// did not finish; its partials are slot 2i + 1 and then slot 2k of
-// k = i + 1, i + 2, ... up to the pair that ends the item, added in that order.
-// Latency counts here: the records of the next 32 pairs come with the first
+// Joins the partials of the items that several parts of the grid share.  CTA
+// (i, y): rows y, y + kPgCombRows, ... of the item that part i of the attention
+// began and did not finish; its partials are slot 2i + 1 and then slot 2k of
+// k = i + 1, i + 2, ... up to the part that ends the item, added in that order.
+// Latency counts here: the records of the next 32 parts come with the first
 // one, and the first partials are loaded before their weights are known.
 constexpr int kPgCombRows = 64;
-__global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PgParams p, int n_pairs) {
+__global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PgParams p, int n_parts) {
   pdl_enter();
   const csa_paged_attn_args& a = p.a;
   const int i = blockIdx.x, lane = threadIdx.x & 31;
   const PgMeta me = p.meta[i];
-  const PgMeta after = i + 1 + lane < n_pairs ? p.meta[i + 1 + lane] : PgMeta{0, 0, 0, 0, 0};
+  const PgMeta after = i + 1 + lane < n_parts ? p.meta[i + 1 + lane] : PgMeta{0, 0, 0, 0, 0};
   if ((int)blockIdx.y >= me.rows) return;
   uint32_t end = __ballot_sync(0xffffffffu, after.cont && after.done);
   int n = __ffs(end) + 1;                      // partials
   for (int k0 = i + 33; !end; k0 += 32) {
-    const PgMeta mk = k0 + lane < n_pairs ? p.meta[k0 + lane] : PgMeta{0, 0, 0, 1, 1};
+    const PgMeta mk = k0 + lane < n_parts ? p.meta[k0 + lane] : PgMeta{0, 0, 0, 1, 1};
     end = __ballot_sync(0xffffffffu, mk.cont && mk.done);
-    n = min(k0 - i + __ffs(end), n_pairs - i);
+    n = min(k0 - i + __ffs(end), n_parts - i);
   }
   auto slot = [&](int s) { return (int64_t)(s == 0 ? 2 * i + 1 : 2 * (i + s)); };
   for (int row = blockIdx.y; row < me.rows; row += kPgCombRows) {
@@ -1224,25 +782,25 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
     float4 v[kR];
 #pragma unroll
     for (int s = 0; s < kR; ++s)
-      v[s] = s < n ? *reinterpret_cast<const float4*>(po + slot(s) * (kPgRows * kD)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[s] = s < n ? *reinterpret_cast<const float4*>(po + slot(s) * (p.item_rows * kD)) : make_float4(0.f, 0.f, 0.f, 0.f);
     const int head = (int)(orow % a.H);
     const float s0 = a.sink ? a.sink[head] * kPgLog2e : -INFINITY;
-    const float2 ml0 = lane < n ? p.part_ml[slot(lane) * kPgRows + row] : make_float2(-INFINITY, 0.f);
+    const float2 ml0 = lane < n ? p.part_ml[slot(lane) * p.item_rows + row] : make_float2(-INFINITY, 0.f);
     float M = ml0.x;
-    for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, p.part_ml[slot(s) * kPgRows + row].x);
+    for (int s = lane + 32; s < n; s += 32) M = fmaxf(M, p.part_ml[slot(s) * p.item_rows + row].x);
     M = warp_max(M);
     M = fmaxf(M - kPgPExp, s0);
     float L = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int sb = 0; sb < n; sb += 32) {
-      const float2 ml = sb == 0 ? ml0 : sb + lane < n ? p.part_ml[slot(sb + lane) * kPgRows + row] : make_float2(-INFINITY, 0.f);
+      const float2 ml = sb == 0 ? ml0 : sb + lane < n ? p.part_ml[slot(sb + lane) * p.item_rows + row] : make_float2(-INFINITY, 0.f);
       const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - kPgPExp - M);
       L += wt * ml.y;
       for (int q = 0; q < 32 && sb + q < n; q += kR) {
         if (sb + q > 0) {
 #pragma unroll
           for (int s = 0; s < kR; ++s)
-            v[s] = sb + q + s < n ? *reinterpret_cast<const float4*>(po + slot(sb + q + s) * (kPgRows * kD)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[s] = sb + q + s < n ? *reinterpret_cast<const float4*>(po + slot(sb + q + s) * (p.item_rows * kD)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
         for (int s = 0; s < kR; ++s) {
@@ -1263,55 +821,71 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
   }
 }
 
-// CTA pairs of a call: one per two SMs, fewer when the call cannot have that
-// many tiles.
-static int pg_pairs(const csa_paged_attn_args* a) {
-  const int64_t items = (a->n_rows * a->H + kPgRows - 1) / kPgRows + a->kv.B;
+// Which kernel a call takes: the one-CTA kernel where the sequences have 64
+// rows or fewer on average, so that most items of 128 would be half empty.
+// 8 x 1 token x 64 heads behind up to 65536 FP8 entries: 118 us by pairs, 76
+// us by single CTAs; 4 x 512 tokens: 2.09 ms and CHUNK ms.
+static bool pg_one(const csa_paged_attn_args* a) { return a->n_rows * a->H <= (int64_t)kPgRows / 2 * a->kv.B; }
+// Parts of the grid (pairs, or CTAs): all SMs, fewer when the call cannot have
+// two tiles for each.
+static int pg_parts(const csa_paged_attn_args* a) {
+  const int rows = pg_one(a) ? kPgRows / 2 : kPgRows, most = pg_one(a) ? kNumSMs : kNumSMs / 2;
+  const int64_t items = (a->n_rows * a->H + rows - 1) / rows + a->kv.B;
   const int64_t tiles = ((int64_t)a->kv.max_pages * a->kv.page_size + kPgE - 1) / kPgE;
-  return items * (tiles + kPgItemCost) / 2 < kNumSMs / 2 ? (int)((items * (tiles + kPgItemCost) + 1) / 2) : kNumSMs / 2;
+  return items * (tiles + kPgItemCost) / 2 < most ? (int)((items * (tiles + kPgItemCost) + 1) / 2) : most;
 }
 static size_t pg_al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// One size rule for both kernels (`slots` partials of 64 rows), so that the
+// workspace of a larger call serves a smaller one.
+static size_t pg_slots(const csa_paged_attn_args* a) { return (size_t)pg_parts(a) * (pg_one(a) ? 2 : 4); }
+
 size_t paged_attn_ws_bytes(const csa_paged_attn_args* a) {
-  const size_t g = (size_t)pg_pairs(a);
-  return pg_al256(g * sizeof(PgMeta)) + pg_al256(g * 2 * kPgRows * sizeof(float2)) + g * 2 * kPgRows * kD * sizeof(float);
+  const size_t n = pg_slots(a);
+  return pg_al256(n / 2 * sizeof(PgMeta)) + pg_al256(n * 64 * sizeof(float2)) + n * 64 * kD * sizeof(float);
+}
+
+cudaError_t launch_paged_attn_one(const PgParams& p, int ctas, cudaStream_t stream);
+
+static cudaError_t launch_pairs(const PgParams& p, int pairs, cudaStream_t stream) {
+  const bool fp4 = p.a.kv.fmt == CSA_FMT_FP4_E2M1_E4M3X16;
+  static SmemAttrOnce attr4, attr8;
+  const cudaError_t e = fp4 ? attr4.set(paged_attn_kernel<true>, kPgSmemBytes) : attr8.set(paged_attn_kernel<false>, kPgSmemBytes);
+  if (e != cudaSuccess) return e;
+  ProfScope ps(stream, "paged_attn");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kPgThreads);
+  cfg.dynamicSmemBytes = kPgSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return fp4 ? cudaLaunchKernelEx(&cfg, paged_attn_kernel<true>, p) : cudaLaunchKernelEx(&cfg, paged_attn_kernel<false>, p);
 }
 
 cudaError_t launch_paged_attn(const csa_paged_attn_args* a, void* ws, cudaStream_t stream) {
-  const bool fp4 = a->kv.fmt == CSA_FMT_FP4_E2M1_E4M3X16;
-  static SmemAttrOnce attr4, attr8;
-  const cudaError_t ea = fp4 ? attr4.set(paged_attn_kernel<true>, kPgSmemBytes) : attr8.set(paged_attn_kernel<false>, kPgSmemBytes);
-  if (ea != cudaSuccess) return ea;
-  const int g = pg_pairs(a);
+  const bool one = pg_one(a);
+  const int g = pg_parts(a);
+  const size_t n = pg_slots(a);
   PgParams p;
   p.a = *a;
   p.scale_log2 = a->softmax_scale * kPgLog2e;
   p.page_inv = pg_inv((uint32_t)a->kv.page_size);
   p.h_inv = pg_inv((uint32_t)a->H);
+  p.item_rows = one ? kPgRows / 2 : kPgRows;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.meta = reinterpret_cast<PgMeta*>(w);
-  w += pg_al256((size_t)g * sizeof(PgMeta));
+  w += pg_al256(n / 2 * sizeof(PgMeta));
   p.part_ml = reinterpret_cast<float2*>(w);
-  w += pg_al256((size_t)g * 2 * kPgRows * sizeof(float2));
+  w += pg_al256(n * 64 * sizeof(float2));
   p.part_o = reinterpret_cast<float*>(w);
-  {
-    ProfScope ps(stream, "paged_attn");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * g);
-    cfg.blockDim = dim3(kPgThreads);
-    cfg.dynamicSmemBytes = kPgSmemBytes;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {2, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    const cudaError_t el = fp4 ? cudaLaunchKernelEx(&cfg, paged_attn_kernel<true>, p) : cudaLaunchKernelEx(&cfg, paged_attn_kernel<false>, p);
-    if (el != cudaSuccess) return el;
-  }
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = one ? launch_paged_attn_one(p, g, stream) : launch_pairs(p, g, stream);
+  if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(stream, "paged_attn_combine");

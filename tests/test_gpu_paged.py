@@ -158,6 +158,122 @@ def test_attention(csa, case):
     _check(out, lse, B.want(window, s))
 
 
+def _thin(lens, H):
+    """The same sequences among enough others without new tokens that a call
+    has at most 64 (token, head) rows per sequence on average, which is where
+    it changes kernels."""
+    rows = sum(n for n, _ in lens) * H
+    return lens + [(0, 3)] * max(0, -(-rows // 64) - len(lens))
+
+
+@pytest.mark.parametrize("case", range(len(SMALL)))
+def test_attention_with_few_rows_per_sequence(csa, case):
+    lens, H, fmt, page, window, sink = SMALL[case]
+    B = Batch(300 + case, _thin(lens, H), H, fmt, page)
+    s = B.sink if sink else None
+    out, lse = _run(csa, B, B.device(csa), window, s, rope=case % 2 == 0)
+    _check(out, lse, B.want(window, s, rope=case % 2 == 0), rope=case % 2 == 0)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("scale", [0.0, 1.0])
+def test_softmax_scales_with_few_rows(csa, fmt, scale):
+    B = Batch(17, _thin([(5, 300), (1, 70)], 16), 16, fmt, 32)
+    out, lse = _run(csa, B, B.device(csa), scale=scale)
+    _check(out, lse, B.want(scale=scale))
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_running_max_with_few_rows(csa, order):
+    B = Batch(18, _thin([(4, 900), (2, 700)], 32), 32, "fp8", 16)
+    rng = np.random.default_rng(3)
+    for b, T in ((0, 900), (1, 700)):
+        gain = np.linspace(0.05, 6.0, T)[::order]
+        e = _encode((rng.standard_normal((T, 512)) * gain[:, None]).astype(np.float32), "fp8")
+        for p in range(0, T, 16):
+            k = min(16, T - p)
+            B.pages[B.table[b, p // 16], :k] = e[p:p + k]
+    out, lse = _run(csa, B, B.device(csa))
+    _check(out, lse, B.want())
+
+
+def test_block_exponents_far_from_one_with_few_rows(csa):
+    B = Batch(19, _thin([(1, 200), (2, 100)], 16), 16, "fp8", 16)
+    flat = B.pages.reshape(-1, 528)
+    rng = np.random.default_rng(4)
+    for p in range(200):
+        row = flat[B.table[0, p // 16] * 16 + p % 16]
+        row[:512] = rng.permutation(np.tile([c for c in range(256) if c & 0x7F != 0x7F], 3))[:512]
+        row[512:] = rng.integers(90, 124, 16)
+    out, lse = _run(csa, B, B.device(csa), scale=0.02)
+    # as in the test above: decoded values on fp16's grid
+    want = B.want(scale=0.02)
+    size = want[3] + 0.02 * 2.0 ** -7 * np.abs(B.q.double().numpy()).sum(-1)
+    _check(out, lse, (want[0], want[1], want[2] + 2.0 ** -13, size, want[4]))
+
+
+def test_few_rows_that_see_nothing(csa):
+    """Tokens before position 0, caches of length 0 and missing pages, single
+    tokens each: zero rows, lse = sink or -inf."""
+    B = Batch(20, [(1, 0), (1, 20), (1, 16), (1, -3), (1, 33)], 16)
+    B.table[1, :] = -1
+    B.table[2, 0] = B.n_pages
+    for sink in (None, B.sink):
+        out, lse = _run(csa, B, B.device(csa), sink=sink)
+        _check(out[4:], lse[4:], [x[4:] for x in B.want(sink=sink)])
+        assert not out[:4].any()
+        ref = torch.full((4, 16), -np.inf) if sink is None else torch.from_numpy(sink).expand(4, 16)
+        assert torch.equal(lse[:4].cpu(), ref) if sink is None else torch.allclose(lse[:4].cpu(), ref, rtol=2 ** -20, atol=0)
+
+
+def test_single_tokens_of_many_sequences_repeat_their_bits(csa):
+    """Split over most of the GPU, sequences of very different lengths, more
+    than 32 of them; twice the same bits."""
+    rng = np.random.default_rng(21)
+    lens = [(1, int(x)) for x in rng.integers(1, 700, 70)] + [(1, 9000), (0, 50), (1, 1)]
+    B = Batch(21, lens, 64, "fp8", 32, tail_rows=2)
+    kv = B.device(csa)
+    out, lse = _run(csa, B, kv, sink=B.sink)
+    _check(out, lse, B.want(sink=B.sink))
+    assert torch.all(out[-2:] == 3.0) and torch.all(lse[-2:] == 3.0)
+    again = _run(csa, B, kv, sink=B.sink)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_single_tokens_in_a_graph(csa):
+    """A decode step captured once and replayed as the caches grow."""
+    B = Batch(22, [(1, 500), (1, 90), (1, 64)], 16, "fp4", 16)
+    kv = B.device(csa)
+    q = B.q.cuda()
+    out = torch.empty((3, 16, 512), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((3, 16), device="cuda")
+    a = csa.paged_attn_args(q=q, kv=kv, out=out, lse=lse, softmax_scale=0.04)
+    ws = torch.empty(csa.csa_paged_attn_workspace_size(a), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        csa.csa_paged_attn(a, workspace=ws)
+    for drop in (0, 37, 63):
+        B.kv = np.array([T - drop for _, T in B.lens], dtype=np.int32)
+        B.d["kv_len"].copy_(torch.from_numpy(B.kv))
+        out.fill_(3.0)
+        lse.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        _check(out, lse, B.want(scale=0.04))
+    assert csa.device_status() == 0
+
+
+def test_workspace_of_a_larger_call_serves_a_smaller_one(csa):
+    B = Batch(23, [(70, 400), (9, 60)], 16, "fp8", 16)
+    kv = B.device(csa)
+    sizes = []
+    for n in (1, 2, 8, 9, 40, 79):
+        q = B.q[:n].cuda()
+        a = csa.paged_attn_args(q=q, kv=kv, out=torch.empty((n, 16, 512), dtype=torch.bfloat16, device="cuda"), softmax_scale=0.04)
+        sizes.append(csa.csa_paged_attn_workspace_size(a))
+    assert sizes == sorted(sizes)
+
+
 @pytest.mark.parametrize("fmt", ["fp8", "fp4"])
 @pytest.mark.parametrize("scale", [0.0, 1e-3, 1.0])
 def test_softmax_scales(csa, fmt, scale):
