@@ -831,14 +831,20 @@ static bool pg_one(const csa_paged_attn_args* a) { return a->n_rows * a->H <= (i
 static int pg_parts(const csa_paged_attn_args* a) {
   const int rows = pg_one(a) ? kPgRows / 2 : kPgRows, most = pg_one(a) ? kNumSMs : kNumSMs / 2;
   const int64_t items = (a->n_rows * a->H + rows - 1) / rows + a->kv.B;
-  const int64_t tiles = ((int64_t)a->kv.max_pages * a->kv.page_size + kPgE - 1) / kPgE;
+  const int e = pg_one(a) ? kPgTile<kPgRows / 2> : kPgTile<kPgRows>;
+  const int64_t tiles = ((int64_t)a->kv.max_pages * a->kv.page_size + e - 1) / e;
   return items * (tiles + kPgItemCost) / 2 < most ? (int)((items * (tiles + kPgItemCost) + 1) / 2) : most;
 }
 static size_t pg_al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// One size rule for both kernels (`slots` partials of 64 rows), so that the
-// workspace of a larger call serves a smaller one.
-static size_t pg_slots(const csa_paged_attn_args* a) { return (size_t)pg_parts(a) * (pg_one(a) ? 2 : 4); }
+// Partials of 64 rows in the workspace: two per CTA of either kernel.  One
+// bound for both that grows with the call, so that the workspace of a larger
+// call serves a smaller one.
+static size_t pg_slots(const csa_paged_attn_args* a) {
+  const int64_t items = (a->n_rows * a->H + 63) / 64 + a->kv.B;
+  const int64_t tiles = ((int64_t)a->kv.max_pages * a->kv.page_size + 31) / 32;
+  return 2 * (size_t)(items * (tiles + kPgItemCost) < kNumSMs ? items * (tiles + kPgItemCost) : kNumSMs);
+}
 
 size_t paged_attn_ws_bytes(const csa_paged_attn_args* a) {
   const size_t n = pg_slots(a);

@@ -4,7 +4,7 @@
 //
 // A work item is up to ROWS query rows (token, head) of one sequence, rows in
 // (token, head) order, so any head count fills it; it runs over the key tiles
-// of kPgE entries that its rows see.
+// of kPgTile entries that its rows see.
 //
 // Work split: the batch is a line on which an item of T key tiles takes
 // kPgItemCost + T; part i of G (a CTA pair, or a CTA) takes the tiles on
@@ -27,7 +27,10 @@
 
 namespace csa {
 
-constexpr int kPgE = 64;                  // entries per key tile
+// Entries per key tile, by an item's rows.
+template <int ROWS>
+constexpr int kPgTile = ROWS == 64 ? 32 : 64;
+constexpr int kPgE = kPgTile<128>;
 constexpr int kPgOwn = 32;                // ... decoded together
 constexpr int kPgQTmemBlocks = 6;         // 64-channel blocks of Q in TMEM
 // warps 0-3: softmax and output
@@ -140,7 +143,8 @@ CSA_DEV void pg_item(const PgParams& p, const PgSeq& s, int j, int& k0, int& k1)
   k0 = a.window ? max(0, p0 + 1 > a.window ? p0 + 1 - a.window : 0) : 0;
   if (k1 < k0) k1 = k0;
 }
-CSA_DEV int pg_tiles(int k0, int k1) { return (k1 - k0 + kPgE - 1) / kPgE; }
+template <int ROWS>
+CSA_DEV int pg_tiles(int k0, int k1) { return (k1 - k0 + kPgTile<ROWS> - 1) / kPgTile<ROWS>; }
 
 // A part's walk over its items.  An item of T key tiles spans kPgItemCost + T
 // of the cost axis; the part takes the tiles whose place lies in its range.
@@ -154,7 +158,7 @@ struct PgWalk {
   int off, take;       // first key tile taken here, number taken
   CSA_DEV void item(const PgParams& p) {
     pg_item<ROWS>(p, s, j, k0, k1);
-    total = pg_tiles(k0, k1);
+    total = pg_tiles<ROWS>(k0, k1);
     off = min(max(at - kPgItemCost, 0), total);
     take = (int)min((int64_t)total, max(at + left - kPgItemCost, (int64_t)0)) - off;
   }
@@ -213,7 +217,7 @@ CSA_DEV int64_t pg_group_cost(const PgParams& p, int g, int lane) {
     for (int j = 0; j < s.tiles; ++j) {
       int k0, k1;
       pg_item<ROWS>(p, s, j, k0, k1);
-      u += kPgItemCost + pg_tiles(k0, k1);
+      u += kPgItemCost + pg_tiles<ROWS>(k0, k1);
     }
   }
   for (uint32_t big = __ballot_sync(0xffffffffu, s.tiles > 4); big; big &= big - 1) {
@@ -227,7 +231,7 @@ CSA_DEV int64_t pg_group_cost(const PgParams& p, int g, int lane) {
     for (int j = lane; j < q.tiles; j += 32) {
       int k0, k1;
       pg_item<ROWS>(p, q, j, k0, k1);
-      v += kPgItemCost + pg_tiles(k0, k1);
+      v += kPgItemCost + pg_tiles<ROWS>(k0, k1);
     }
     v = pg_warp_sum64(v);
     if (lane == l) u = v;
@@ -297,7 +301,7 @@ CSA_DEV void pg_plan(const PgParams& p, int64_t* gsum, int64_t* start, int part,
         if (j + lane < s.tiles) {
           int k0, k1;
           pg_item<ROWS>(p, s, j + lane, k0, k1);
-          w = kPgItemCost + pg_tiles(k0, k1);
+          w = kPgItemCost + pg_tiles<ROWS>(k0, k1);
         }
         const int64_t sum = pg_warp_sum64(w);
         if (at < sum || j + 32 >= s.tiles) {

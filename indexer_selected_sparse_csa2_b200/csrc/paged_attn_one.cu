@@ -2,40 +2,41 @@
 // each, where the pair kernel's items of 128 rows would stay half empty (a new
 // token of 64 heads, or of 16, is one such item).
 //
-// Per key tile of 64 entries, K = V = the decoded entries:
+// Per key tile of 32 entries, K = V = the decoded entries:
 //   S = Q K^T       M = 128 TMEM lanes holding the 64 rows twice (lane L: row L
-//                   mod 64), N = 2 x 32 entries, K = 512.  Channels 0..383 of Q
-//                   are the A operand in TMEM, the last 128 in shared memory.
-//                   Lanes 0..63 go on with the first 32 entries, lanes 64.. with
-//                   the others.
-//   O^T += V^T P^T  M = 128 channels (4 chunks), N = 64 rows, K = 64 entries: 4
+//                   mod 64), N = 32 entries, K = 512.  Channels 0..383 of Q are
+//                   the A operand in TMEM, the last 128 in shared memory.  The
+//                   two copies let two pairs of softmax warps take turns.
+//   O^T += V^T P^T  M = 128 channels (4 chunks), N = 64 rows, K = 32 entries: 4
 //                   x 64 TMEM columns, where O (64 x 512) would take all 512.
 // An entry is decoded once; its shared-memory copy is the K-major B operand of
 // S and the MN-major A operand of O^T, where the pair kernel's CTAs keep two
-// tiles and decode half of the other's channels as well.  Entries move in half
-// tiles of 32 through a ring of five: group g of the decode warps fills half g
-// of each tile, a buffer is free when the tile's PV has retired.
+// tiles and decode half of the other's channels as well.
 //
-// Bound: the tensor pipe and shared memory alike, about 2200 cycles a tile (S
-// 24 x 32 + 8 x 80, O^T 16 x 48; 64 KB written, 208 KB read).
+// Bound: the tensor pipe and shared memory alike, about 1100 cycles a tile (S
+// 24 x 16 + 8 x 40, O^T 8 x 48; 32 KB written, 104 KB read).  Five tiles are in
+// flight, because a tile's way (decode, S, softmax, PV) is five times as long;
+// with tiles of 64 entries, two and a half of them, a tile took 3600 cycles
+// instead of twice PERIOD.
 #include "paged_attn.cuh"
 
 namespace csa {
 
 constexpr int kP1Rows = 64;
-constexpr int kP1Bufs = 5;                // half tiles in flight
+constexpr int kP1E = kPgTile<kP1Rows>;    // entries per key tile
+constexpr int kP1Bufs = 5;                // tiles in flight
 constexpr int kP1QBlk = 128 * 128;        // shared Q block: 128 rows x 64 fp16
-constexpr int kP1PBytes = kP1Rows * kPgE * 2;
-constexpr size_t kP1SmemBytes = 2 * kP1QBlk + kP1Bufs * kPgKBytes + 2 * kP1PBytes + 3072;
+constexpr int kP1PBytes = kP1Rows * kP1E * 2;
+constexpr size_t kP1SmemBytes = 2 * kP1QBlk + kP1Bufs * (kPgKBytes + kP1PBytes) + 3072;
 static_assert(kP1SmemBytes <= 232448, "shared memory of a CTA");
 static_assert(kPgMaxB / 32 * 8 <= kP1Bufs * kPgKBytes, "the plan's group sums use the entry tiles");
 
 struct P1Smem {
   uint8_t* q;        // channels 384..511 of Q: 2 blocks
   uint8_t* kv;       // [kP1Bufs] 32 entries, 8 blocks of 64 channels
-  uint8_t* p;        // [2] P tiles
-  float* mx;         // [2][2][64] tile maxima by tile parity and entry half
-  float* lx;         // [2][64] sums by entry half
+  uint8_t* p;        // [kP1Bufs] P tiles
+  float* mx;         // [2][64] tile maxima by tile parity
+  float* lx;         // [2][64] sums over the even and the odd tiles
   float* alpha;      // [64] rescale factors
   float* scl;        // [64] output factors
   uint32_t* valid;   // [kP1Bufs] entries present
@@ -48,8 +49,8 @@ CSA_DEV P1Smem carve_p1(uint8_t* p) {
   P1Smem s;
   s.q = p; p += 2 * kP1QBlk;
   s.kv = p; p += kP1Bufs * kPgKBytes;
-  s.p = p; p += 2 * kP1PBytes;
-  s.mx = reinterpret_cast<float*>(p); p += 4 * 64 * 4;
+  s.p = p; p += kP1Bufs * kP1PBytes;
+  s.mx = reinterpret_cast<float*>(p); p += 2 * 64 * 4;
   s.lx = reinterpret_cast<float*>(p); p += 2 * 64 * 4;
   s.alpha = reinterpret_cast<float*>(p); p += 64 * 4;
   s.scl = reinterpret_cast<float*>(p); p += 64 * 4;
@@ -75,22 +76,32 @@ CSA_DEV void p1_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t ides
       ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "n"(ACC ? 1 : 0) : "memory");
 }
 
+// P rows are 64 bytes (32 fp16): 64-byte swizzle for that operand.
+constexpr uint32_t kP1DescP = (512u >> 4) | 1u << 14 | 4u << 29;
+template <bool ACC>
+CSA_DEV void p1_mma_pv(uint32_t d, uint32_t v_lo, uint32_t p_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
+      ::"r"(d), "r"(v_lo), "r"(p_lo), "r"(idesc), "n"(kPgDesc), "n"(kP1DescP), "n"(ACC ? 1 : 0) : "memory");
+}
+
 template <bool FP4>
 __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __grid_constant__ PgParams p) {
   constexpr int kScaleOff = FP4 ? 256 : 512;
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const P1Smem S = carve_p1(smem_raw);
-  // h = 2 t + half counts half tiles; buffer h % kP1Bufs
+  // tile t: buffer t % kP1Bufs, S tile t & 1
   uint64_t* kv_full = S.bars + 0;    // [kP1Bufs] decoded (4 warp arrivals)
-  uint64_t* kv_free = S.bars + 5;    // [kP1Bufs] the tile's PV done (commit)
-  uint64_t* s_full = S.bars + 10;    // S in TMEM (commit)
-  uint64_t* s_free = S.bars + 11;    // S read by the softmax (4)
-  uint64_t* p_full = S.bars + 12;    // [2] P written, O^T rescaled (4)
-  uint64_t* q_full = S.bars + 14;    // an item's Q staged (8)
-  uint64_t* q_free = S.bars + 15;    // an item's last S done (commit)
-  uint64_t* acc_done = S.bars + 16;  // an item's last PV done (commit)
-  uint64_t* drain = S.bars + 17;     // [2] all MMAs of an issuer retired (teardown)
+  uint64_t* kv_free = S.bars + 5;    // [kP1Bufs] PV done: buffer and P tile reusable (commit)
+  uint64_t* p_full = S.bars + 10;    // [kP1Bufs] P written, O^T rescaled (2)
+  uint64_t* s_full = S.bars + 15;    // [2] S in TMEM (commit)
+  uint64_t* s_free = S.bars + 17;    // [2] S read by the softmax (2)
+  uint64_t* q_full = S.bars + 19;    // an item's Q staged (8)
+  uint64_t* q_free = S.bars + 20;    // an item's last S done (commit)
+  uint64_t* acc_done = S.bars + 21;  // an item's last PV done (commit)
+  uint64_t* drain = S.bars + 22;     // [2] all MMAs of an issuer retired (teardown)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = blockIdx.x, parts = gridDim.x;
   const csa_paged_attn_args& a = p.a;
@@ -98,13 +109,13 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
     for (int k = 0; k < kP1Bufs; ++k) {
       mbar_init(kv_full + k, 4);
       mbar_init(kv_free + k, 1);
+      mbar_init(p_full + k, 2);
     }
     for (int k = 0; k < 2; ++k) {
-      mbar_init(p_full + k, 4);
+      mbar_init(s_full + k, 1);
+      mbar_init(s_free + k, 2);
       mbar_init(drain + k, 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 4);
     mbar_init(q_full, 8);
     mbar_init(q_free, 1);
     mbar_init(acc_done, 1);
@@ -120,7 +131,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
 
   if (warp == kPgWarpS) {
     // ------------------------------------------------------------ S issuer
-    constexpr uint32_t idesc = idesc_make(kFmtF16, kFmtF16, 128, kPgOwn);
+    constexpr uint32_t idesc = idesc_make(kFmtF16, kFmtF16, 128, kP1E);
     const uint32_t qd = pg_desc_k(smem_u32(S.q)), kd0 = pg_desc_k(smem_u32(S.kv));
     PgWalk<kP1Rows> w;
     uint32_t t = 0, seg = 0;
@@ -129,30 +140,25 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
       if (w.take == 0) continue;
       ok = pg_wait_warp(q_full, seg++ & 1u, kErrWaitTmaFull);
       for (int i = 0; i < w.take && ok; ++i, ++t) {
-        if (t >= 1) ok = pg_wait_warp(s_free, (t - 1) & 1u, kErrWaitAccEmpty);
+        const uint32_t si = t & 1u, bi = t % kP1Bufs;
+        if (t >= 2) ok = pg_wait_warp(s_free + si, ((t >> 1) - 1) & 1u, kErrWaitAccEmpty);
+        ok = ok && pg_wait_warp(kv_full + bi, (t / kP1Bufs) & 1u, kErrWaitTmaFull);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t kd = kd0 + bi * (kPgKBytes >> 4), sd = tbase + kPgSCol + kP1E * si;
+        if (pg_elect()) {
+          p1_mma_ts<false>(sd, tbase, kd, idesc);
 #pragma unroll
-        for (uint32_t half = 0; half < 2; ++half) {
-          const uint32_t h = 2 * t + half, bi = h % kP1Bufs;
-          ok = ok && pg_wait_warp(kv_full + bi, (h / kP1Bufs) & 1u, kErrWaitTmaFull);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t kd = kd0 + bi * (kPgKBytes >> 4), sd = tbase + kPgSCol + 32 * half;
-          if (pg_elect()) {
-            p1_mma_ts<false>(sd, tbase, kd, idesc);
-#pragma unroll
-            for (int ks = 1; ks < kD / 16; ++ks) {
-              const uint32_t kb = ks >> 2, sub = ks & 3;
-              const uint32_t bd = kd + kb * (kPgKBlk >> 4) + sub * 2;
-              if (kb < (uint32_t)kPgQTmemBlocks) p1_mma_ts<true>(sd, tbase + kb * 32 + sub * 8, bd, idesc);
-              else p1_mma_ss<true>(sd, qd + (kb - kPgQTmemBlocks) * (kP1QBlk >> 4) + sub * 2, bd, idesc);
-            }
-            if (half == 1) {
-              mma_commit(s_full);
-              if (i == w.take - 1) mma_commit(q_free);
-            }
+          for (int ks = 1; ks < kD / 16; ++ks) {
+            const uint32_t kb = ks >> 2, sub = ks & 3;
+            const uint32_t bd = kd + kb * (kPgKBlk >> 4) + sub * 2;
+            if (kb < (uint32_t)kPgQTmemBlocks) p1_mma_ts<true>(sd, tbase + kb * 32 + sub * 8, bd, idesc);
+            else p1_mma_ss<true>(sd, qd + (kb - kPgQTmemBlocks) * (kP1QBlk >> 4) + sub * 2, bd, idesc);
           }
-          __syncwarp();
+          mma_commit(s_full + si);
+          if (i == w.take - 1) mma_commit(q_free);
         }
+        __syncwarp();
       }
     }
     if (pg_elect()) mma_commit(drain);
@@ -166,24 +172,22 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
     bool ok = true;
     for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
       for (int i = 0; i < w.take; ++i, ++t) {
-        ok = pg_wait_warp(p_full + (t & 1u), (t >> 1) & 1u, kErrWaitAccFull);
+        const uint32_t bi = t % kP1Bufs;
+        ok = pg_wait_warp(p_full + bi, (t / kP1Bufs) & 1u, kErrWaitAccFull);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t b0 = (2 * t) % kP1Bufs, b1 = (2 * t + 1) % kP1Bufs;
-        const uint32_t v0 = vd0 + b0 * (kPgKBytes >> 4), v1 = vd0 + b1 * (kPgKBytes >> 4);
-        const uint32_t pd = pd0 + (t & 1u) * (kP1PBytes >> 4);
+        const uint32_t vd = vd0 + bi * (kPgKBytes >> 4), pd = pd0 + bi * (kP1PBytes >> 4);
         if (pg_elect()) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
 #pragma unroll
-            for (int ks = 0; ks < kPgE / 16; ++ks) {
-              const uint32_t ad = (ks < 2 ? v0 : v1) + 2 * c * (kPgKBlk >> 4) + (ks & 1) * (2048 >> 4), bd = pd + ks * 2;
-              if (ks == 0 && i == 0) p1_mma_ss<false>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
-              else p1_mma_ss<true>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
+            for (int ks = 0; ks < kP1E / 16; ++ks) {
+              const uint32_t ad = vd + 2 * c * (kPgKBlk >> 4) + ks * (2048 >> 4), bd = pd + ks * 2;
+              if (ks == 0 && i == 0) p1_mma_pv<false>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
+              else p1_mma_pv<true>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
             }
           }
-          mma_commit(kv_free + b0);
-          mma_commit(kv_free + b1);
+          mma_commit(kv_free + bi);
           if (i == w.take - 1) mma_commit(acc_done);
         }
         __syncwarp();
@@ -193,7 +197,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
     __syncwarp();
   } else if (warp >= kPgWarpDec) {
     // ---------------------------------------------- entry loads and decoding
-    // Warp wq of group g takes entries 32 g + 8 wq .. of every tile.
+    // Group g (4 warps) takes the CTA's tiles of parity g, 8 entries a warp.
     const int wq = (warp - kPgWarpDec) & 3, g = (warp - kPgWarpDec) >> 2;
     // the first item's query rows come first: their way is the longest
     PgWalk<kP1Rows> w;
@@ -202,15 +206,15 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
     auto rows = [&]() { return PgRowsIn{w.s.row0, w.j * kP1Rows, min(w.s.n * a.H - w.j * kP1Rows, kP1Rows)}; };
     if (go) pg_fetch_q(p, rows(), S.kv + g * kPgKBytes, wq, lane, g);
     PgCursor<kP1Rows> cu;              // the tile whose page table values are fetched next
-    cu.begin(p, S.start, 0);
-    // page id and entry number in the page of entry 32 g + 8 wq + (lane & 7) of
-    // the tile whose entries are loaded next
+    cu.begin(p, S.start, g);
+    // page id and entry number in the page of entry 8 wq + (lane & 7) of the
+    // tile whose entries are loaded next
     int id = -1;
     uint32_t slot = 0;
     auto lookup = [&]() {
       id = -1;
       if (cu.live) {
-        const int pos = cu.w.k0 + (cu.w.off + cu.i) * kPgE + kPgOwn * g + 8 * wq + (lane & 7);
+        const int pos = cu.w.k0 + (cu.w.off + cu.i) * kP1E + 8 * wq + (lane & 7);
         if (pos < cu.w.k1) {
           int rem;
           const int pg = pg_div(pos, a.kv.page_size, p.page_inv, rem);
@@ -258,32 +262,32 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
     };
     lookup();
     load_tile();
-    cu.advance(p, 1);
+    cu.advance(p, 2);
     lookup();
     const uint32_t kv_at = smem_u32(S.kv) + (uint32_t)kb * kPgKBlk;
-    uint32_t t = 0, seg = 0;
+    uint32_t t0 = 0, seg = 0;          // tiles before the item, items with tiles before it
     bool ok = true;
     // a failed wait leaves `ok` false and skips the later waits and all work;
     // every warp still passes its group's barriers once per item
     for (; go; go = w.next(p)) {
       if (w.take == 0) continue;
       const PgRowsIn R = rows();
-      // the raw rows go through the buffer of the group's next half tile
-      uint32_t h = 2 * t + g;
-      uint8_t* q_buf = S.kv + (h % kP1Bufs) * kPgKBytes;
+      // the raw rows go through the buffer of the group's next tile
+      uint32_t t = t0 + ((t0 ^ (uint32_t)g) & 1u);
+      uint8_t* q_buf = S.kv + (t % kP1Bufs) * kPgKBytes;
       if (seg > 0) {
         ok = ok && pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty);
-        if (ok && h >= kP1Bufs) ok = pg_wait_warp(kv_free + h % kP1Bufs, (h / kP1Bufs - 1) & 1u, kErrWaitSmemEmpty);
+        if (ok && t >= kP1Bufs) ok = pg_wait_warp(kv_free + t % kP1Bufs, (t / kP1Bufs - 1) & 1u, kErrWaitSmemEmpty);
         if (ok) pg_fetch_q(p, R, q_buf, wq, lane, g);
       }
       tc_fence_after();
       pg_stage_q<true>(p, R, q_buf, S.q, tbase, wq, lane, g, ok);
       if (ok && lane == 0) mbar_arrive(q_full);
       ++seg;
-      for (int i = 0; i < w.take; ++i, ++t) {
-        h = 2 * t + g;
-        const uint32_t bi = h % kP1Bufs;
-        if (ok && h >= kP1Bufs) ok = pg_wait_warp(kv_free + bi, (h / kP1Bufs - 1) & 1u, kErrWaitSmemEmpty);
+      t0 += (uint32_t)w.take;
+      for (; t < t0; t += 2) {
+        const uint32_t bi = t % kP1Bufs;
+        if (ok && t >= kP1Bufs) ok = pg_wait_warp(kv_free + bi, (t / kP1Bufs - 1) & 1u, kErrWaitSmemEmpty);
         if (!ok) continue;
         const uint32_t kt = kv_at + bi * kPgKBytes;
         auto put = [&](int row, int c, const uint4& q) {    // 8 channels of an entry
@@ -338,15 +342,18 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
         // the next tile's entries, all loads together, then the table values
         // of the tile after it
         load_tile();
-        cu.advance(p, 1);
+        cu.advance(p, 2);
         lookup();
       }
     }
   } else {
     // ------------------------------------------------------ softmax, output
-    const int q4 = warp, rr = 32 * (q4 & 1) + lane;          // TMEM lane quarter, row
-    const int half = q4 >> 1;                                // entries 32 half .. of a tile
-    const uint32_t trow = tbase + ((uint32_t)(32 * q4) << 16);
+    // Warps 0-1 take the CTA's even tiles, warps 2-3 the odd ones: while one
+    // pair turns its S into P, the other reads the next S and finds its max.
+    // All four meet once per tile, where the running max may move.
+    const int rr = 32 * (warp & 1) + lane;     // row of the item
+    const uint32_t grp = (uint32_t)warp >> 1;
+    const uint32_t trow = tbase + ((uint32_t)(32 * warp) << 16);
     // scale 0: logits 0 with factor 1, since -inf * 0 is not a number
     const bool zero = p.scale_log2 == 0.f;
     const float sc = zero ? 1.f : p.scale_log2;
@@ -362,47 +369,49 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
       const int tok = pg_div(w.j * kP1Rows + rr, a.H, p.h_inv, head);
       const int hi = rr < n_on ? w.s.kv - w.s.n + tok : -1;
       const int lo = a.window && hi >= a.window ? hi - a.window : -1;
-      float m_run = -INFINITY, l_run = 0.f;    // l_run: this lane's entry half
+      float m_run = -INFINITY, l_run = 0.f;    // l_run: this pair's tiles
       for (int i = 0; i < nt; ++i, ++t) {
-        const uint32_t si = t & 1u;
-        const int kb = w.k0 + (w.off + i) * kPgE + 32 * half;
-        const int nh = hi - kb + 1, nl = lo - kb + 1;        // the row sees entries [nl, nh) of this half
-        uint32_t mask = nh >= 32 ? 0xffffffffu : nh <= 0 ? 0u : (1u << nh) - 1u;
-        mask &= nl <= 0 ? 0xffffffffu : nl >= 32 ? 0u : ~((1u << nl) - 1u);
+        const uint32_t bi = t % kP1Bufs, si = t & 1u;
+        const bool own = si == grp;
+        uint32_t sv[32];
+        float mt = -INFINITY;
         // a failed wait leaves `ok` false and skips the later waits; every
         // warp still passes the group's barriers once per tile
-        ok = ok && pg_wait_warp(s_full, si, kErrWaitAccFull);
-        tc_fence_after();
-        uint32_t sv[32];
-        tmem_ld32(trow + kPgSCol + 32 * half, sv);
-        mask &= S.valid[(2 * t + half) % kP1Bufs];           // written before the tile's S was issued
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
-        if (zero) {
+        if (own) {
+          const int kb = w.k0 + (w.off + i) * kP1E;
+          const int nh = hi - kb + 1, nl = lo - kb + 1;      // the row sees entries [nl, nh) of the tile
+          uint32_t mask = nh >= 32 ? 0xffffffffu : nh <= 0 ? 0u : (1u << nh) - 1u;
+          mask &= nl <= 0 ? 0xffffffffu : nl >= 32 ? 0u : ~((1u << nl) - 1u);
+          ok = ok && pg_wait_warp(s_full + si, (t >> 1) & 1u, kErrWaitAccFull);
+          tc_fence_after();
+          tmem_ld32(trow + kPgSCol + kP1E * si, sv);
+          mask &= S.valid[bi];                 // written before the tile's S was issued
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free + si);
+          if (zero) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) sv[k] = 0u;
+            for (int k = 0; k < 32; ++k) sv[k] = 0u;
+          }
+          if (!__all_sync(0xffffffffu, mask == 0xffffffffu)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sv[k] = ((mask >> k) & 1u) ? sv[k] : 0xff800000u;   // -inf
+          }
+          float m4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(__uint_as_float(sv[k]), __uint_as_float(sv[k + 4]));
+#pragma unroll
+          for (int k = 8; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(sv[k]));
+          mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          if (mt != -INFINITY) mt *= sc;
+          S.mx[64 * si + rr] = mt;
         }
-        if (!__all_sync(0xffffffffu, mask == 0xffffffffu)) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) sv[k] = ((mask >> k) & 1u) ? sv[k] : 0xff800000u;   // -inf
-        }
-        float m4[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = fmaxf(__uint_as_float(sv[k]), __uint_as_float(sv[k + 4]));
-#pragma unroll
-        for (int k = 8; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(sv[k]));
-        float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        if (mt != -INFINITY) mt *= sc;
-        S.mx[(2 * si + half) * 64 + rr] = mt;
         uint32_t over;
-        // O^T has a row in a column, which all four warps hold a part of: they
-        // all meet
         asm volatile("{\n .reg .pred q, r;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred r, 1, 128, q;\n selp.u32 %0, 1, 0, r;\n}"
                      : "=r"(over) : "r"(mt > m_run + kPgRescale ? 1u : 0u) : "memory");
         if (over) {
-          const float mm = fmaxf(mt, S.mx[(2 * si + (half ^ 1)) * 64 + rr]);
+          const float mm = S.mx[64 * si + rr];
           float alpha = 1.f;
           if (mm > m_run + kPgRescale) {
             alpha = m_run == -INFINITY ? 0.f : pg_ex2(m_run - mm);
@@ -410,11 +419,11 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
             l_run *= alpha;
           }
           if (i > 0) {
-            if (half == 0) S.alpha[rr] = alpha;
-            named_bar(2, 128);
-            // O^T, once the PV before this tile's has retired
-            const uint32_t hp = 2 * t - 1;
-            ok = ok && pg_wait_warp(kv_free + hp % kP1Bufs, (hp / kP1Bufs) & 1u, kErrWaitAccFull);
+            if (own) S.alpha[rr] = alpha;
+            named_bar(1, 128);
+            // O^T (a row is a column of it, in all four warps' lanes), once the
+            // PV before this tile's has retired
+            ok = ok && pg_wait_warp(kv_free + (t - 1) % kP1Bufs, ((t - 1) / kP1Bufs) & 1u, kErrWaitAccFull);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 256; c += 16) {
@@ -433,42 +442,46 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
               tmem_st16(trow + kPgOCol + c, o);
             }
             tmem_wait_st();
+            tc_fence_before();
+            named_bar(1, 128);                 // every quarter rescaled before this tile's PV
           }
         }
-        // the P tile is free once the PV two tiles back has retired
-        if (t >= 2) ok = ok && pg_wait_warp(kv_free + (2 * t - 3) % kP1Bufs, ((2 * t - 3) / kP1Bufs) & 1u, kErrWaitSmemEmpty);
-        // a row that has seen nothing yet: every logit here is -inf, and so is
-        // its max; any finite reference gives the zeros it needs
-        const float mref = m_run == -INFINITY ? 0.f : m_run - kPgPExp;
-        float l0 = 0.f, l1 = 0.f;
-        uint8_t* pt = S.p + si * kP1PBytes;
+        if (own) {
+          // this tile's P buffer is free: its entries were decoded after the
+          // PV that read both last.  A row that has seen nothing yet: every
+          // logit here is -inf, and so is its max; any finite reference gives
+          // the zeros it needs
+          const float mref = m_run == -INFINITY ? 0.f : m_run - kPgPExp;
+          float l0 = 0.f, l1 = 0.f;
+          uint8_t* pt = S.p + bi * kP1PBytes;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[4];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e0 = 8 * c + 2 * k;
-            const float x0 = pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref));
-            const float x1 = pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref));
-            l0 += x0;
-            l1 += x1;
-            o[k] = pg_h2u(__floats2half2_rn(x0, x1));
+            for (int k = 0; k < 4; ++k) {
+              const int e0 = 8 * c + 2 * k;
+              const float x0 = pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref));
+              const float x1 = pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref));
+              l0 += x0;
+              l1 += x1;
+              o[k] = pg_h2u(__floats2half2_rn(x0, x1));
+            }
+            *reinterpret_cast<uint4*>(pt + sw64_offset(rr, 16 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          *reinterpret_cast<uint4*>(pt + sw128_offset_h(rr, 32 * half + 8 * c)) = make_uint4(o[0], o[1], o[2], o[3]);
+          l_run += l0 + l1;
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + bi);
         }
-        l_run += l0 + l1;
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + si);
       }
       // ------------------------------------------------------------ output
       const bool whole = w.take == w.total;
-      S.lx[half * 64 + rr] = l_run;
+      S.lx[64 * grp + rr] = l_run;
       named_bar(1, 128);
       const int64_t orow = (int64_t)w.s.row0 * a.H + w.j * kP1Rows;
       const int slot = 2 * part + (w.off > 0 ? 0 : 1);
-      if (half == 0) {
+      if (grp == 0) {
         const float l = S.lx[rr] + S.lx[64 + rr];
         float scl = 1.f;
         if (whole) {
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
       const bool valid_o = nt > 0 && ok;
 #pragma unroll 1
       for (int c = 0; c < 256; c += 32) {                    // rows (c & 32) .. of channels 2 c ..
-        const int k0 = c & 32, ch = 2 * (c & ~63) + 32 * q4 + lane;
+        const int k0 = c & 32, ch = 2 * (c & ~63) + 32 * warp + lane;
         if (k0 >= n_on) continue;
         uint32_t o[32];
         if (valid_o) {
@@ -512,7 +525,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
           for (int k = 0; k < 32; ++k)
             if (k0 + k < n_on) dst[k * kD] = __uint_as_float(o[k]);
         } else {
-          const bool rope = a.rope_cs && c >= 192 && q4 >= 2;  // channels 448 ..: pairs in neighbouring lanes
+          const bool rope = a.rope_cs && c >= 192 && warp >= 2;  // channels 448 ..: pairs in neighbouring lanes
           const int odd = lane & 1;
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (orow + k0 + odd) * kD + (ch & ~1);
 #pragma unroll
