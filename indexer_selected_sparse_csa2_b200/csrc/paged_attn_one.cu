@@ -24,6 +24,12 @@ namespace csa {
 
 constexpr int kP1Rows = 64;
 constexpr int kP1E = kPgTile<kP1Rows>;    // entries per key tile
+// Warp roles are the pair kernel's, with a second S issuer: 12 and 14, for even
+// and odd tiles.  A warp goes on behind a commit only when its MMAs are about
+// done, so one alone issued a tile's S every 1630 cycles.  (In the pair kernel
+// S would then delay PV: 2.36 ms for 2.11.)
+constexpr int kP1Threads = kPgThreads + 32;
+constexpr int kP1WarpS2 = kPgWarps;
 constexpr int kP1Bufs = 5;                // tiles in flight
 constexpr int kP1QBlk = 128 * 128;        // shared Q block: 128 rows x 64 fp16
 constexpr int kP1PBytes = kP1Rows * kP1E * 2;
@@ -54,7 +60,7 @@ CSA_DEV P1Smem carve_p1(uint8_t* p) {
   s.lx = reinterpret_cast<float*>(p); p += 2 * 64 * 4;
   s.alpha = reinterpret_cast<float*>(p); p += 64 * 4;
   s.scl = reinterpret_cast<float*>(p); p += 64 * 4;
-  s.bars = reinterpret_cast<uint64_t*>(p); p += 24 * 8;
+  s.bars = reinterpret_cast<uint64_t*>(p); p += 26 * 8;
   s.start = reinterpret_cast<int64_t*>(p); p += 4 * 8;
   s.valid = reinterpret_cast<uint32_t*>(p); p += 8 * 4;
   s.tmem_base = reinterpret_cast<uint32_t*>(p);
@@ -87,7 +93,7 @@ CSA_DEV void p1_mma_pv(uint32_t d, uint32_t v_lo, uint32_t p_lo, uint32_t idesc)
 }
 
 template <bool FP4>
-__global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __grid_constant__ PgParams p) {
+__global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __grid_constant__ PgParams p) {
   constexpr int kScaleOff = FP4 ? 256 : 512;
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -99,9 +105,9 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
   uint64_t* s_full = S.bars + 15;    // [2] S in TMEM (commit)
   uint64_t* s_free = S.bars + 17;    // [2] S read by the softmax (2)
   uint64_t* q_full = S.bars + 19;    // an item's Q staged (8)
-  uint64_t* q_free = S.bars + 20;    // an item's last S done (commit)
+  uint64_t* q_free = S.bars + 20;    // an item's S all done (2 commits)
   uint64_t* acc_done = S.bars + 21;  // an item's last PV done (commit)
-  uint64_t* drain = S.bars + 22;     // [2] all MMAs of an issuer retired (teardown)
+  uint64_t* drain = S.bars + 22;     // [3] all MMAs of an issuer retired (teardown)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int part = blockIdx.x, parts = gridDim.x;
   const csa_paged_attn_args& a = p.a;
@@ -114,33 +120,35 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
     for (int k = 0; k < 2; ++k) {
       mbar_init(s_full + k, 1);
       mbar_init(s_free + k, 2);
-      mbar_init(drain + k, 1);
     }
+    for (int k = 0; k < 3; ++k) mbar_init(drain + k, 1);
     mbar_init(q_full, 8);
-    mbar_init(q_free, 1);
+    mbar_init(q_free, 2);
     mbar_init(acc_done, 1);
     fence_mbar_init();
   }
   if (warp == kPgWarpS) tmem_alloc(S.tmem_base, kPgTmemCols);
   pdl_wait();
-  pg_plan<kP1Rows>(p, reinterpret_cast<int64_t*>(S.kv), S.start, part, parts, warp, kPgWarps, lane);
+  pg_plan<kP1Rows>(p, reinterpret_cast<int64_t*>(S.kv), S.start, part, parts, warp, kP1Threads / 32, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *S.tmem_base;
 
-  if (warp == kPgWarpS) {
+  if (warp == kPgWarpS || warp == kP1WarpS2) {
     // ------------------------------------------------------------ S issuer
     constexpr uint32_t idesc = idesc_make(kFmtF16, kFmtF16, 128, kP1E);
+    const uint32_t mine = warp == kPgWarpS ? 0u : 1u;        // parity of this issuer's tiles
     const uint32_t qd = pg_desc_k(smem_u32(S.q)), kd0 = pg_desc_k(smem_u32(S.kv));
     PgWalk<kP1Rows> w;
-    uint32_t t = 0, seg = 0;
+    uint32_t t0 = 0, seg = 0;
     bool ok = true;
     for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
       if (w.take == 0) continue;
       ok = pg_wait_warp(q_full, seg++ & 1u, kErrWaitTmaFull);
-      for (int i = 0; i < w.take && ok; ++i, ++t) {
-        const uint32_t si = t & 1u, bi = t % kP1Bufs;
+      const uint32_t end = t0 + (uint32_t)w.take;
+      for (uint32_t t = t0 + ((t0 ^ mine) & 1u); t < end && ok; t += 2) {
+        const uint32_t si = mine, bi = t % kP1Bufs;
         if (t >= 2) ok = pg_wait_warp(s_free + si, ((t >> 1) - 1) & 1u, kErrWaitAccEmpty);
         ok = ok && pg_wait_warp(kv_full + bi, (t / kP1Bufs) & 1u, kErrWaitTmaFull);
         if (!ok) break;
@@ -156,12 +164,14 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
             else p1_mma_ss<true>(sd, qd + (kb - kPgQTmemBlocks) * (kP1QBlk >> 4) + sub * 2, bd, idesc);
           }
           mma_commit(s_full + si);
-          if (i == w.take - 1) mma_commit(q_free);
         }
         __syncwarp();
       }
+      t0 = end;
+      if (ok && pg_elect()) mma_commit(q_free);
+      __syncwarp();
     }
-    if (pg_elect()) mma_commit(drain);
+    if (pg_elect()) mma_commit(drain + mine);
     __syncwarp();
   } else if (warp == kPgWarpPV) {
     // ----------------------------------------------------------- PV issuer
@@ -193,7 +203,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
         __syncwarp();
       }
     }
-    if (pg_elect()) mma_commit(drain + 1);
+    if (pg_elect()) mma_commit(drain + 2);
     __syncwarp();
   } else if (warp >= kPgWarpDec) {
     // ---------------------------------------------- entry loads and decoding
@@ -569,6 +579,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_one_kernel(const __g
     // every MMA issued has retired before TMEM and shared memory go
     pg_wait_warp(drain, 0u, kErrWaitAccFull);
     pg_wait_warp(drain + 1, 0u, kErrWaitAccFull);
+    pg_wait_warp(drain + 2, 0u, kErrWaitAccFull);
     tc_fence_after();
     tmem_dealloc(tbase, kPgTmemCols);
   }
@@ -580,8 +591,8 @@ cudaError_t launch_paged_attn_one(const PgParams& p, int ctas, cudaStream_t stre
   const cudaError_t e = fp4 ? attr4.set(paged_attn_one_kernel<true>, kP1SmemBytes) : attr8.set(paged_attn_one_kernel<false>, kP1SmemBytes);
   if (e != cudaSuccess) return e;
   ProfScope ps(stream, "paged_attn");
-  if (fp4) launch_k(paged_attn_one_kernel<true>, dim3(ctas), dim3(kPgThreads), kP1SmemBytes, stream, p);
-  else launch_k(paged_attn_one_kernel<false>, dim3(ctas), dim3(kPgThreads), kP1SmemBytes, stream, p);
+  if (fp4) launch_k(paged_attn_one_kernel<true>, dim3(ctas), dim3(kP1Threads), kP1SmemBytes, stream, p);
+  else launch_k(paged_attn_one_kernel<false>, dim3(ctas), dim3(kP1Threads), kP1SmemBytes, stream, p);
   return cudaGetLastError();
 }
 
