@@ -67,7 +67,7 @@ struct PgSmem {
   float* mx;         // [2][2][64] tile maxima by tile parity and entry half
   float* lx;         // [2][64] sums by entry half
   uint32_t* valid;   // [kPgVBufs][2] entries present, by entry half
-  int64_t* start;    // the pair's range: {its start inside its first item, length, sequence, item}
+  int64_t* start;    // the pair's range: {its start inside its first item, length, sequence, item, PgSeq}
   uint64_t* bars;
   uint32_t* tmem_base;
 };
@@ -81,7 +81,7 @@ CSA_DEV PgSmem carve_pg(uint8_t* p) {
   s.mx = reinterpret_cast<float*>(p); p += 4 * 64 * 4;
   s.lx = reinterpret_cast<float*>(p); p += 2 * 64 * 4;
   s.bars = reinterpret_cast<uint64_t*>(p); p += 24 * 8;
-  s.start = reinterpret_cast<int64_t*>(p); p += 4 * 8;
+  s.start = reinterpret_cast<int64_t*>(p); p += 8 * 8;
   s.valid = reinterpret_cast<uint32_t*>(p); p += 2 * kPgVBufs * 4;
   s.tmem_base = reinterpret_cast<uint32_t*>(p);
   return s;
@@ -754,19 +754,19 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 }
 
 // Joins the partials of the items that several parts of the grid share.  CTA
-// (i, y): rows y, y + kPgCombRows, ... of the item that part i of the attention
-// began and did not finish; its partials are slot 2i + 1 and then slot 2k of
+// (i, y): rows of the item that part i of the attention began and did not
+// finish, 128 threads a row; its partials are slot 2i + 1 and then slot 2k of
 // k = i + 1, i + 2, ... up to the part that ends the item, added in that order.
 // Latency counts here: the records of the next 32 parts come with the first
 // one, and the first partials are loaded before their weights are known.
-constexpr int kPgCombRows = 64;
-__global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_constant__ PgParams p, int n_parts) {
+constexpr int kPgCombRows = 4, kPgCombY = 16;   // rows of a CTA, CTAs of a part
+__global__ void __launch_bounds__(128 * kPgCombRows) paged_attn_combine_kernel(const __grid_constant__ PgParams p, int n_parts) {
   pdl_enter();
   const csa_paged_attn_args& a = p.a;
-  const int i = blockIdx.x, lane = threadIdx.x & 31;
+  const int i = blockIdx.x, lane = threadIdx.x & 31, col = threadIdx.x & 127;
   const PgMeta me = p.meta[i];
   const PgMeta after = i + 1 + lane < n_parts ? p.meta[i + 1 + lane] : PgMeta{0, 0, 0, 0, 0};
-  if ((int)blockIdx.y >= me.rows) return;
+  if ((int)blockIdx.y * kPgCombRows >= me.rows) return;
   uint32_t end = __ballot_sync(0xffffffffu, after.cont && after.done);
   int n = __ffs(end) + 1;                      // partials
   for (int k0 = i + 33; !end; k0 += 32) {
@@ -775,9 +775,9 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
     n = min(k0 - i + __ffs(end), n_parts - i);
   }
   auto slot = [&](int s) { return (int64_t)(s == 0 ? 2 * i + 1 : 2 * (i + s)); };
-  for (int row = blockIdx.y; row < me.rows; row += kPgCombRows) {
+  for (int row = blockIdx.y * kPgCombRows + (threadIdx.x >> 7); row < me.rows; row += kPgCombRows * kPgCombY) {
     const int64_t orow = me.row0 + row;
-    const float* po = p.part_o + (int64_t)row * kD + 4 * threadIdx.x;
+    const float* po = p.part_o + (int64_t)row * kD + 4 * col;
     constexpr int kR = 8;
     float4 v[kR];
 #pragma unroll
@@ -814,10 +814,10 @@ __global__ void __launch_bounds__(128) paged_attn_combine_kernel(const __grid_co
     const bool any = L > 0.f;
     if (s0 != -INFINITY) L += exp2f(s0 - M);
     const float f = any ? 1.f / L : 0.f;
-    if (threadIdx.x == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kPgLn2 : -INFINITY;
+    if (col == 0 && a.lse) a.lse[orow] = L > 0.f ? (M + log2f(L)) * kPgLn2 : -INFINITY;
     const float* cs = a.rope_cs ? a.rope_cs + orow / a.H * 64 : nullptr;
-    store_out4(a.out, true, orow * kD + 4 * threadIdx.x,
-               rope_out4(make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f), cs, 4 * threadIdx.x));
+    store_out4(a.out, true, orow * kD + 4 * col,
+               rope_out4(make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f), cs, 4 * col));
   }
 }
 
@@ -895,7 +895,7 @@ cudaError_t launch_paged_attn(const csa_paged_attn_args* a, void* ws, cudaStream
   if (e != cudaSuccess) return e;
   {
     ProfScope ps(stream, "paged_attn_combine");
-    launch_k(paged_attn_combine_kernel, dim3(g, kPgCombRows), dim3(128), 0, stream, p, g);
+    launch_k(paged_attn_combine_kernel, dim3(g, kPgCombY), dim3(128 * kPgCombRows), 0, stream, p, g);
   }
   note_launches(2);
   return cudaGetLastError();

@@ -187,7 +187,10 @@ struct PgWalk {
     b = (int)start[2];
     j = (int)start[3];
     if (left <= 0) return false;
-    s = pg_seq<ROWS>(p.a, b);
+    s.n = (int)start[4];
+    s.kv = (int)start[5];
+    s.row0 = (int)start[6];
+    s.tiles = (int)start[7];
     item(p);
     settle(p);
     return left > 0;
@@ -282,6 +285,7 @@ CSA_DEV void pg_plan(const PgParams& p, int64_t* gsum, int64_t* start, int part,
     }
     int64_t at = u0;
     int b = 0, j = 0;
+    PgSeq s{0, 0, 0, 0};
     if (u1 > u0) {
       int base = 0;
       for (; groups > 1; base += 32) {                     // the 32 groups
@@ -295,7 +299,7 @@ CSA_DEV void pg_plan(const PgParams& p, int64_t* gsum, int64_t* start, int part,
       }
       const int64_t v = groups > 1 ? pg_group_cost<ROWS>(p, base, lane) : only;   // the sequence
       b = 32 * base + pg_locate(v, at, lane);
-      const PgSeq s = pg_seq<ROWS>(a, b);
+      s = pg_seq<ROWS>(a, b);
       for (;; j += 32) {                                   // the item
         int64_t w = 0;
         if (j + lane < s.tiles) {
@@ -316,6 +320,10 @@ CSA_DEV void pg_plan(const PgParams& p, int64_t* gsum, int64_t* start, int part,
       start[1] = u1 - u0;
       start[2] = b;
       start[3] = j;
+      start[4] = s.n;
+      start[5] = s.kv;
+      start[6] = s.row0;
+      start[7] = s.tiles;
     }
   }
   __syncthreads();

@@ -61,7 +61,7 @@ CSA_DEV P1Smem carve_p1(uint8_t* p) {
   s.alpha = reinterpret_cast<float*>(p); p += 64 * 4;
   s.scl = reinterpret_cast<float*>(p); p += 64 * 4;
   s.bars = reinterpret_cast<uint64_t*>(p); p += 26 * 8;
-  s.start = reinterpret_cast<int64_t*>(p); p += 4 * 8;
+  s.start = reinterpret_cast<int64_t*>(p); p += 8 * 8;
   s.valid = reinterpret_cast<uint32_t*>(p); p += 8 * 4;
   s.tmem_base = reinterpret_cast<uint32_t*>(p);
   return s;
