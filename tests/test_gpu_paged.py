@@ -403,6 +403,21 @@ def test_page_offsets_past_32_bits(csa):
     del buf, pages
 
 
+@pytest.mark.parametrize("H", [16, 128])
+def test_positions_up_to_two_to_the_31(csa, H):
+    """The last positions a table can have, behind a window: tiles that end
+    past 2^31."""
+    n = 2 ** 31 - 1
+    B = Batch(26, [(1, 200)], H, "fp8", 1)
+    B.device(csa)
+    table = torch.empty((1, n), dtype=torch.int32, device="cuda")          # only its end is read
+    table[0, n - 200:] = B.d["block_table"][0, :200]
+    kv = csa.paged_kv(pages=B.d["pages"], block_table=table, cu_q=B.d["cu_q"],
+                      kv_len=torch.tensor([n], dtype=torch.int32, device="cuda"))
+    out, lse = _run(csa, B, kv, window=90)
+    _check(out, lse, B.want(window=90))
+
+
 def test_same_bits_on_every_run(csa):
     B = Batch(17, [(1, 4000), (30, 500), (1, 2)], 64, "fp8", 64)
     kv = B.device(csa)
