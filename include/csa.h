@@ -264,9 +264,9 @@ csa_status csa_sparse_attn(const csa_attn_args* a, void* workspace, size_t works
  *     CSA_SCALE_UE8M0X32: per 32 channels the exponent byte e + 127 with e
  *                         the smallest integer with amax <= 448 * 2^e,
  *                         clamped to [-127, 127]; code = E4M3_rne_sat(y * 2^-e)
- *     CSA_SCALE_F32X128 : per 128 channels the fp32 scale amax / 448;
- *                         code = E4M3_rne_sat(y * (1 / scale)); a zero scale
- *                         gives zero codes
+ *     CSA_SCALE_F32X128 : per 128 channels the fp32 scale amax / 448, at
+ *                         least 2^-126, or 0 for a block of zeros, whose codes
+ *                         are 0; code = E4M3_rne_sat(y * (1 / scale))
  * y enters the codes unrounded.  x, residual, residual_out and out share one
  * type; residual_out and out may be x or residual themselves (same pointer
  * and stride), any other overlap is outside the contract.  Non-finite inputs

@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(WARP_ROW ? 256 : 512) rms_norm_kernel(const __
       } else if (p.scale_kind == CSA_SCALE_F32X128) {
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const float sc = __fdiv_rn(amax, 448.f);
+        // at least 2^-126, whose reciprocal fp32 holds
+        const float sc = amax > 0.f ? fmaxf(__fdiv_rn(amax, 448.f), 0x1p-126f) : 0.f;
         inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
         if ((lane & 15) == 0 && ch < chunks) static_cast<float*>(p.scales)[r * p.scales_stride + (ch >> 4)] = sc;
       }

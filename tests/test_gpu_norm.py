@@ -121,6 +121,25 @@ def test_norm_without_weight_and_with_zero_rows_of_channels(csa):
     _check_codes(codes[2:3], sc[2:3], y[2:3], "ue8m0", "tiny")
 
 
+def test_norm_of_rows_whose_scales_have_no_reciprocal(csa):
+    """amax / 448 below 2^-127, zeros beside it: codes stay within half a step
+    of y / 2^-126 (E4M3's smallest step is 2^-9)."""
+    x = torch.zeros(3, 256, device="cuda")
+    x[0, 0], x[0, 1], x[0, 130] = 2.0 ** -125, -(2.0 ** -128), 2.0 ** -121
+    x[1, 5] = 2.0 ** -140
+    w = torch.ones(256, device="cuda")
+    codes = torch.empty(3, 256, dtype=torch.uint8, device="cuda")
+    scales = torch.full((3, 2), 9.0, device="cuda")
+    csa.csa_rms_norm(csa.rms_norm_args(x=x, weight=w, eps=1.0, codes=codes, scales=scales))
+    torch.cuda.synchronize()
+    want = _f64(x)                                   # mean(x^2) is nothing beside eps = 1
+    v = codecs.e4m3_decode(codes.cpu().numpy())
+    s = _f64(scales)
+    assert np.array_equal(s, [[2.0 ** -126, 2.0 ** -126], [2.0 ** -126, 0.0], [0.0, 0.0]])
+    z = want / 2.0 ** -126
+    assert np.all(np.abs(v - z) <= np.maximum(2.0 ** -4 * np.abs(z), 2.0 ** -10) + 2.0 ** -17)
+
+
 def test_norm_in_place_and_strided(csa):
     rows, dim = 37, 640
     for dt in (torch.float32, torch.bfloat16):
