@@ -269,8 +269,8 @@ csa_status csa_sparse_attn(const csa_attn_args* a, void* workspace, size_t works
  *                         are 0; code = E4M3_rne_sat(y * (1 / scale))
  * y enters the codes unrounded.  x, residual, residual_out and out share one
  * type; residual_out and out may be x or residual themselves (same pointer
- * and stride), any other overlap is outside the contract.  Non-finite inputs
- * are outside the contract. */
+ * and stride), any other overlap is outside the contract.  Non-finite inputs,
+ * and a row of zeros with eps = 0, are outside the contract. */
 typedef enum { CSA_SCALE_NONE = 0, CSA_SCALE_UE8M0X32 = 1, CSA_SCALE_F32X128 = 2 } csa_scale_kind;
 
 typedef struct {
@@ -354,7 +354,13 @@ csa_status csa_paged_append(const csa_paged_append_args* a, csa_stream_t stream)
  * sink).  One new token per sequence is the decode step, kv_len[b] = n_b a
  * whole prompt, anything between a chunk; sequences of a call may differ.
  * Entries must decode to |x| < 65504 and queries hold |q| < 65504 (fp16
- * operands, fp32 accumulation); rotated queries are rounded to fp16. */
+ * operands, fp32 accumulation); rotated queries are rounded to fp16.  An entry
+ * that does not (NaN codes, a scale past the range) may spoil any row of its
+ * sequence in the call, also one whose mask leaves it out; entries that no row
+ * of the call sees are not looked at, whatever their bytes.  A query that does
+ * not spoils its own row.
+ * The workspace holds partial results from the call to its end: calls that may
+ * run at the same time (two streams, two captured graphs) need one each. */
 typedef struct {
   csa_paged_kv kv;
   const void* q;             /* bf16, row i head h at q + i*q_row_stride + h*q_head_stride elements */
@@ -362,7 +368,7 @@ typedef struct {
   int64_t q_row_stride;      /* elements, multiples of 8 */
   int64_t q_head_stride;     /* elements, >= 512, a multiple of 8 */
   int32_t H, D;              /* H in 1..128; D must be 512 */
-  float softmax_scale;       /* >= 0, finite */
+  float softmax_scale;       /* 0..1e30 */
   int32_t window;            /* 0: no window; else >= 1 */
   const float* sink;         /* optional fp32 [H] sink logits */
   const float* rope_cs;      /* optional fp32 [n_rows][32][2]: q rotated forward, out back */

@@ -358,7 +358,9 @@ def csa_paged_attn(args: PagedAttnArgs, workspace=None, stream=None, device=None
     # the library checks a given workspace's size itself; query it only to allocate one
     if workspace is None:
         dev = getattr(args, "_device", None)
-        workspace = _workspace(csa_paged_attn_workspace_size(args), device or ("cuda" if dev is None else f"cuda:{dev}"))
+        where = device or ("cuda" if dev is None else f"cuda:{dev}")
+        with _torch().cuda.stream(stream):          # its memory is the stream's: freed here, reused behind the call
+            workspace = _workspace(csa_paged_attn_workspace_size(args), where)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _on_device(args, stream, lambda st: _paged_attn(args, _ptr(workspace), nbytes, st), "csa_paged_attn")
 

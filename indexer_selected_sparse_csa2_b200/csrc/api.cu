@@ -202,7 +202,7 @@ static csa_status check_paged_attn(const csa_paged_attn_args* a) {
   if (a->n_rows < 0 || a->n_rows >= ((int64_t)1 << 31) || a->n_rows * a->H >= ((int64_t)1 << 30)) return CSA_ERR_SHAPE;
   if (a->n_rows == 0) return CSA_OK;
   if (!a->q || !a->out) return CSA_ERR_INVALID_ARG;
-  if (!(a->softmax_scale >= 0.f) || !(a->softmax_scale <= 3.0e38f)) return CSA_ERR_INVALID_ARG;
+  if (!(a->softmax_scale >= 0.f) || !(a->softmax_scale <= 1.0e30f)) return CSA_ERR_INVALID_ARG;
   if (a->q_head_stride < kD || a->q_row_stride < 0) return CSA_ERR_SHAPE;
   if (!al16(a->q) || !al16i(a->q_row_stride * 2) || !al16i(a->q_head_stride * 2) || !al16(a->out) || !al16(a->rope_cs))
     return CSA_ERR_ALIGNMENT;

@@ -470,6 +470,51 @@ def test_graph_replay_follows_the_lengths(csa):
         _check(out, lse, B.want())
 
 
+def test_workspace_of_a_call_on_another_stream(csa):
+    """Calls without a workspace, on a stream that is not the current one: the
+    memory they allocate stays theirs until they are done."""
+    B = Batch(27, [(1, 6000), (1, 40)], 64, "fp8", 64)
+    kv = B.device(csa)
+    want = _run(csa, B, kv)
+    q, side = B.q.cuda(), torch.cuda.Stream()
+    out, lse = torch.empty(2, 64, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 64, device="cuda")
+    a = csa.paged_attn_args(q=q, kv=kv, out=out, lse=lse, softmax_scale=512 ** -0.5)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        csa.csa_paged_attn(a, stream=side)
+        for _ in range(4):                           # takes and writes what the current stream may have
+            torch.full((csa.csa_paged_attn_workspace_size(a),), 0xFF, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("H", [16, 128])
+def test_bytes_of_entries_that_no_row_sees(csa, H, fmt):
+    """NaN codes and scales behind the sequences' ends, before the windows and
+    in pages of no sequence change no bit."""
+    B = Batch(28, [(1, 300), (3, 77), (1, 1)], H, fmt, 16)
+    first = _run(csa, B, B.device(csa), window=50)
+    _check(*first, B.want(window=50))
+    seen = np.zeros(B.pages.shape[:2], dtype=bool)
+    for b, (n, T) in enumerate(B.lens):
+        for p in range(max(0, T - n - 49), T):
+            seen[B.table[b, p // 16], p % 16] = True
+    B.pages[~seen] = 0xFF
+    again = _run(csa, B, B.device(csa), window=50)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("H", [2, 128])
+def test_more_than_a_thousand_sequences(csa, H):
+    """The plan's sums over groups of sequences, in both kernels."""
+    rng = np.random.default_rng(29)
+    lens = [(int(n), int(n) + int(T)) for n, T in zip(rng.integers(0, 3, 1100), rng.integers(0, 90, 1100))]
+    B = Batch(29, lens, H, "fp4", 16)
+    out, lse = _run(csa, B, B.device(csa), sink=B.sink)
+    _check(out, lse, B.want(sink=B.sink))
+
+
 # -------------------------------------------------------------------- append
 def _append(csa, B, src, n_rows=None, **kw):
     kv = B.device(csa)
@@ -592,3 +637,45 @@ def test_norm_append_attention_as_a_layer_uses_them(csa):
         s = np.repeat(np.ldexp(1.0, raw[:, 512:].astype(int) - 127), 32, axis=1)
         err = np.abs(fp8_window_dequant_rows(raw) - y)
         assert np.all(err <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * s) + 2.0 ** -17 * np.abs(y))
+
+
+def test_norm_append_attention_in_a_graph(csa):
+    """The same chain for a decode step, captured once and replayed while the
+    caches grow by a token a step, against the chain call by call."""
+    lens = [(1, 60), (1, 30), (1, 77)]
+    res = []
+    for graph in (False, True):
+        B = Batch(30, lens, 16, "fp8", 16)
+        kv = B.device(csa)
+        gen = torch.Generator(device="cuda").manual_seed(5)
+        src = torch.randn(3, 512, generator=gen, device="cuda")
+        y, q = torch.empty_like(src), B.q.cuda()
+        w = torch.rand(512, generator=gen, device="cuda") + 0.5
+        cs = torch.from_numpy(B.cs).cuda()
+        out, lse = torch.empty(3, 16, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 16, device="cuda")
+        n = csa.rms_norm_args(x=src, out=y, weight=w)
+        p = csa.paged_append_args(src=y, kv=kv, norm=True, weight=w, rope_cs=cs)
+        a = csa.paged_attn_args(q=q, kv=kv, out=out, lse=lse, softmax_scale=0.04, rope_cs=cs)
+        ws = torch.empty(csa.csa_paged_attn_workspace_size(a), dtype=torch.uint8, device="cuda")
+
+        def step():
+            csa.csa_rms_norm(n)
+            csa.csa_paged_append(p)
+            csa.csa_paged_attn(a, workspace=ws)
+
+        got = []
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g):
+                step()
+        for i in range(4):
+            g.replay() if graph else step()
+            torch.cuda.synchronize()
+            got.append((out.clone(), lse.clone(), B.d["pages"].clone()))
+            B.d["kv_len"].add_(1)
+            src.mul_(-1.5)
+        res.append(got)
+    for one, two in zip(*res):
+        assert all(torch.equal(u, v) for u, v in zip(one, two))
+    assert csa.device_status() == 0

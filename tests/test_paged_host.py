@@ -176,6 +176,17 @@ def test_paged_attn_refusals(csa):
     assert csa._paged_attn(None, None, 0, None) == I and csa._paged_attn_ws(None) == 0
 
 
+def test_paged_attn_scale_stays_where_its_product_with_log2_e_is_finite(csa):
+    a = csa.PagedAttnArgs()
+    _kv(csa, a.kv)
+    a.q = a.out = 4096
+    a.n_rows, a.H, a.D, a.q_row_stride, a.q_head_stride = 5, 16, 512, 16 * 512, 512
+    for scale, want in ((1e30, csa.CSA_ERR_WORKSPACE), (0.0, csa.CSA_ERR_WORKSPACE), (2e30, csa.CSA_ERR_INVALID_ARG),
+                        (2.9e38, csa.CSA_ERR_INVALID_ARG)):
+        a.softmax_scale = scale
+        assert csa._paged_attn(ctypes.byref(a), None, 0, None) == want
+
+
 def test_argument_builders_check_types_and_shapes(csa):
     z = torch.zeros
     with pytest.raises(TypeError):
