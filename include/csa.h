@@ -318,7 +318,7 @@ typedef struct {
   int64_t page_stride;       /* bytes, a multiple of 16 */
   const int32_t* block_table;  /* [B][max_pages], row b at block_table + b * table_stride */
   int64_t table_stride;      /* elements, >= max_pages */
-  int32_t max_pages;         /* 1 <= max_pages, max_pages * page_size < 2^31 */
+  int32_t max_pages;         /* 1 <= max_pages, max_pages * page_size <= 2^31 - 128 */
   int32_t B;                 /* sequences, 1..65536 */
   const int32_t* cu_q;       /* [B + 1] */
   const int32_t* kv_len;     /* [B] */

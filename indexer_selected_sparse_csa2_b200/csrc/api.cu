@@ -170,7 +170,8 @@ static csa_status check_norm(const csa_norm_args* a) {
 static csa_status check_paged(const csa_paged_kv* k) {
   if (k->fmt != CSA_FMT_FP4_E2M1_E4M3X16 && k->fmt != CSA_FMT_FP8_E4M3_UE8M0X32) return CSA_ERR_INVALID_ARG;
   if (k->B < 1 || k->B > 65536 || k->page_size < 1 || k->page_size > 65536 || k->max_pages < 1) return CSA_ERR_SHAPE;
-  if ((int64_t)k->max_pages * k->page_size >= ((int64_t)1 << 31)) return CSA_ERR_SHAPE;
+  // a tile behind the last position still has 32-bit positions
+  if ((int64_t)k->max_pages * k->page_size > ((int64_t)1 << 31) - 128) return CSA_ERR_SHAPE;
   if (k->n_pages < 1 || k->n_pages >= ((int64_t)1 << 31) || k->table_stride < k->max_pages) return CSA_ERR_SHAPE;
   if (!k->pages || !k->block_table || !k->cu_q || !k->kv_len) return CSA_ERR_INVALID_ARG;
   const int64_t bytes = k->fmt == CSA_FMT_FP4_E2M1_E4M3X16 ? kFp4Bytes : kFp8Bytes;

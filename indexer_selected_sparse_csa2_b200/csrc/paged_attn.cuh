@@ -143,9 +143,8 @@ CSA_DEV void pg_item(const PgParams& p, const PgSeq& s, int j, int& k0, int& k1)
   k0 = a.window ? max(0, p0 + 1 > a.window ? p0 + 1 - a.window : 0) : 0;
   if (k1 < k0) k1 = k0;
 }
-// (unsigned: k1 - k0 may be 2^31 - 1)
 template <int ROWS>
-CSA_DEV int pg_tiles(int k0, int k1) { return (int)(((uint32_t)(k1 - k0) + kPgTile<ROWS> - 1) / kPgTile<ROWS>); }
+CSA_DEV int pg_tiles(int k0, int k1) { return (k1 - k0 + kPgTile<ROWS> - 1) / kPgTile<ROWS>; }
 
 // A part's walk over its items.  An item of T key tiles spans kPgItemCost + T
 // of the cost axis; the part takes the tiles whose place lies in its range.

@@ -224,11 +224,10 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
     auto lookup = [&]() {
       id = -1;
       if (cu.live) {
-        // (unsigned: the last tile's end may lie behind 2^31)
-        const uint32_t pos = (uint32_t)cu.w.k0 + (uint32_t)(cu.w.off + cu.i) * kP1E + (uint32_t)(8 * wq + (lane & 7));
-        if (pos < (uint32_t)cu.w.k1) {
+        const int pos = cu.w.k0 + (cu.w.off + cu.i) * kP1E + 8 * wq + (lane & 7);
+        if (pos < cu.w.k1) {
           int rem;
-          const int pg = pg_div((int)pos, a.kv.page_size, p.page_inv, rem);
+          const int pg = pg_div(pos, a.kv.page_size, p.page_inv, rem);
           slot = (uint32_t)rem;
           id = a.kv.block_table[(int64_t)cu.w.b * a.kv.table_stride + pg];
         }

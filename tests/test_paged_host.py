@@ -187,6 +187,17 @@ def test_paged_attn_scale_stays_where_its_product_with_log2_e_is_finite(csa):
         assert csa._paged_attn(ctypes.byref(a), None, 0, None) == want
 
 
+def test_tables_stay_a_tile_below_two_to_the_31_positions(csa):
+    a = csa.PagedAttnArgs()
+    _kv(csa, a.kv)
+    a.q = a.out = 4096
+    a.n_rows, a.H, a.D, a.q_row_stride, a.q_head_stride, a.softmax_scale = 5, 16, 512, 16 * 512, 512, 0.05
+    a.kv.page_size = 1
+    for pages, want in ((2 ** 31 - 128, csa.CSA_ERR_WORKSPACE), (2 ** 31 - 127, csa.CSA_ERR_SHAPE), (2 ** 31 - 1, csa.CSA_ERR_SHAPE)):
+        a.kv.max_pages = a.kv.table_stride = pages
+        assert csa._paged_attn(ctypes.byref(a), None, 0, None) == want
+
+
 def test_argument_builders_check_types_and_shapes(csa):
     z = torch.zeros
     with pytest.raises(TypeError):
