@@ -352,16 +352,16 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         q1 = p1 + (lane >> 2) * rs;
         const uint8_t* o = p0 + (FP4 ? (lane >> 4) * rs + 16 * (lane & 15) : 16 * lane);
 #pragma unroll
-        for (int k = 0; k < kN; ++k, o += (FP4 ? 2 : 1) * rs) r[k] = ld_nc_v4(o);
+        for (int k = 0; k < kN; ++k, o += (FP4 ? 2 : 1) * rs) r[k] = pg_ld_entry<true>(o);
         o = p1 + (FP4 ? lane >> 3 : lane >> 4) * rs + x_off;
 #pragma unroll
-        for (int k = 0; k < kN / 2; ++k, o += (FP4 ? 4 : 2) * rs) x[k] = ld_nc_v4(o);
+        for (int k = 0; k < kN / 2; ++k, o += (FP4 ? 4 : 2) * rs) x[k] = pg_ld_entry<true>(o);
       } else {
 #pragma unroll
         for (int k = 0; k < kN; ++k)
-          r[k] = ld_nc_v4(at_lane(ptr, FP4 ? 2 * k + (lane >> 4) : k) + 16 * (FP4 ? lane & 15 : lane));
+          r[k] = pg_ld_entry<true>(at_lane(ptr, FP4 ? 2 * k + (lane >> 4) : k) + 16 * (FP4 ? lane & 15 : lane));
 #pragma unroll
-        for (int k = 0; k < kN / 2; ++k) x[k] = ld_nc_v4(at_lane(ptr, 8 + (FP4 ? 4 * k + (lane >> 3) : 2 * k + (lane >> 4))) + x_off);
+        for (int k = 0; k < kN / 2; ++k) x[k] = pg_ld_entry<true>(at_lane(ptr, 8 + (FP4 ? 4 * k + (lane >> 3) : 2 * k + (lane >> 4))) + x_off);
         q0 = at_lane(ptr, lane >> 2);
         q1 = at_lane(ptr, 8 + (lane >> 2));
       }

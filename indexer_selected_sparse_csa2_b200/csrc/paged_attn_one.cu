@@ -259,11 +259,11 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
         q0 = p0 + (lane >> 2) * rs;
         const uint8_t* o = p0 + (FP4 ? (lane >> 4) * rs + 16 * (lane & 15) : 16 * lane);
 #pragma unroll
-        for (int k = 0; k < kN; ++k, o += (FP4 ? 2 : 1) * rs) r[k] = ld_nc_v4(o);
+        for (int k = 0; k < kN; ++k, o += (FP4 ? 2 : 1) * rs) r[k] = pg_ld_entry<false>(o);
       } else {
 #pragma unroll
         for (int k = 0; k < kN; ++k)
-          r[k] = ld_nc_v4(at_lane(ptr, FP4 ? 2 * k + (lane >> 4) : k) + 16 * (FP4 ? lane & 15 : lane));
+          r[k] = pg_ld_entry<false>(at_lane(ptr, FP4 ? 2 * k + (lane >> 4) : k) + 16 * (FP4 ? lane & 15 : lane));
         q0 = at_lane(ptr, lane >> 2);
       }
       // scales: lane 4e + w holds word w of entry e's scale bytes
