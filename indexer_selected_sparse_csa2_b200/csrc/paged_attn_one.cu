@@ -143,10 +143,13 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
     PgWalk<kP1Rows> w;
     uint32_t t0 = 0, seg = 0;
     bool ok = true;
-    for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
+    w.open(p, S.start);
+#pragma unroll 1
+    while (ok && w.go(p)) {
       if (w.take == 0) continue;
       ok = pg_wait_warp(q_full, seg++ & 1u, kErrWaitTmaFull);
       const uint32_t end = t0 + (uint32_t)w.take;
+#pragma unroll 1
       for (uint32_t t = t0 + ((t0 ^ mine) & 1u); t < end && ok; t += 2) {
         const uint32_t si = mine, bi = t % kP1Bufs;
         if (t >= 2) ok = pg_wait_warp(s_free + si, ((t >> 1) - 1) & 1u, kErrWaitAccEmpty);
@@ -180,7 +183,10 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
     PgWalk<kP1Rows> w;
     uint32_t t = 0;
     bool ok = true;
-    for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
+    w.open(p, S.start);
+#pragma unroll 1
+    while (ok && w.go(p)) {
+#pragma unroll 1
       for (int i = 0; i < w.take; ++i, ++t) {
         const uint32_t bi = t % kP1Bufs;
         ok = pg_wait_warp(p_full + bi, (t / kP1Bufs) & 1u, kErrWaitAccFull);
@@ -211,8 +217,10 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
     const int wq = (warp - kPgWarpDec) & 3, g = (warp - kPgWarpDec) >> 2;
     // the first item's query rows come first: their way is the longest
     PgWalk<kP1Rows> w;
-    bool go = w.begin(p, S.start);
-    while (go && w.take == 0) go = w.next(p);
+    w.open(p, S.start);
+    bool go = w.go(p);
+#pragma unroll 1
+    while (go && w.take == 0) go = w.go(p);
     auto rows = [&]() { return PgRowsIn{w.s.row0, w.j * kP1Rows, min(w.s.n * a.H - w.j * kP1Rows, kP1Rows)}; };
     if (go) pg_fetch_q(p, rows(), S.kv + g * kPgKBytes, wq, lane, g);
     PgCursor<kP1Rows> cu;              // the tile whose page table values are fetched next
@@ -279,7 +287,8 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
     bool ok = true;
     // a failed wait leaves `ok` false and skips the later waits and all work;
     // every warp still passes its group's barriers once per item
-    for (; go; go = w.next(p)) {
+#pragma unroll 1
+    for (; go; go = w.go(p)) {
       if (w.take == 0) continue;
       const PgRowsIn R = rows();
       // the raw rows go through the buffer of the group's next tile
@@ -295,6 +304,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
       if (ok && lane == 0) mbar_arrive(q_full);
       ++seg;
       t0 += (uint32_t)w.take;
+#pragma unroll 1
       for (; t < t0; t += 2) {
         const uint32_t bi = t % kP1Bufs;
         if (ok && t >= kP1Bufs) ok = pg_wait_warp(kv_free + bi, (t / kP1Bufs - 1) & 1u, kErrWaitSmemEmpty);
@@ -372,7 +382,9 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
     bool ok = true;
     int64_t meta_row0 = 0;
     int meta_rows = 0, meta_cont = 0, meta_done = 0;
-    for (bool go = w.begin(p, S.start); go; go = w.next(p)) {
+    w.open(p, S.start);
+#pragma unroll 1
+    while (w.go(p)) {
       const int nt = w.take, n_on = min(w.s.n * a.H - w.j * kP1Rows, kP1Rows);
       // positions this row sees: (lo, hi]; none for rows past the item's
       int head;
@@ -380,6 +392,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
       const int hi = rr < n_on ? w.s.kv - w.s.n + tok : -1;
       const int lo = a.window && hi >= a.window ? hi - a.window : -1;
       float m_run = -INFINITY, l_run = 0.f;    // l_run: this pair's tiles
+#pragma unroll 1
       for (int i = 0; i < nt; ++i, ++t) {
         const uint32_t bi = t % kP1Bufs, si = t & 1u;
         const bool own = si == grp;
