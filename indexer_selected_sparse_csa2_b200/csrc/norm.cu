@@ -9,7 +9,10 @@
 //   dim <= 1024 : one warp per row (no shared memory, no barrier).
 //   else        : one CTA of dim / (8 C) threads per row.
 // CTAs stay for several rows and load the next one before they reduce this
-// one, so that loads are in flight through the barrier and the stores.
+// one, so that loads are in flight through the barrier and the stores (8192
+// rows of 4096 bf16 channels with residual and UE8M0 codes: 48.9 -> 41.7 us).
+// Measured: those rows 5.66 TB/s, 65537 fp32 rows of 512 channels 5.6 TB/s (48
+// us); one row 6.2 us, a launch.
 #include <algorithm>
 
 #include "common.cuh"

@@ -21,28 +21,24 @@
 //
 // Why two CTAs: shared memory bounds this attention.  With O (64 x 512) of one
 // CTA alone, an entry's 1 KB is written once and read twice for 64 rows; the
-// pair reads half of it per CTA for 128 rows.  A one-CTA kernel of the same
-// roles (32-entry tiles, 64 rows) measured 3.55 ms on 4 x 512 new tokens x 64
-// heads behind up to 16384 FP8 entries; its MMAs alone need 148 KB of shared-
+// pair reads half of it per CTA for 128 rows.  Single CTAs (paged_attn_one.cu)
+// take 3.42 ms where the pairs take 2.30: their MMAs need 148 KB of shared-
 // memory reads and writes per 64 x 32 tile, 84 KB per 64 x 32 here.
-//
-// Online softmax in the exp2 domain; the running max moves only when a tile's
-// max exceeds it by more than 8, and only then O is rescaled in TMEM.  P is
-// held in fp16 times 2^6: at most 2^14, and weights down to 2^-31 of the max
-// keep a value.
-//
-// Work split: the batch is a line on which an item of T key tiles takes
-// kPgItemCost + T; pair i takes the tiles on [iU/G, (i+1)U/G) of its length U,
-// whatever the sequences' lengths, and computes where that is from the lengths
-// on the device.  An item that ends up in several pairs leaves (max, sum, O)
-// partials in the workspace, at most two per pair, which paged_attn_combine
-// joins in order; the result does not depend on timing.
 //
 // Warp roles: 0-3 softmax and output; 4-7 and 8-11 staging of Q, and loading
 // and decoding of even and odd tiles; 12 issues the S MMAs, 13 the PV MMAs (of
-// CTA 0 for both).  In flight: two K tiles, four V tiles, two S and two P.  A
-// second softmax warpgroup left 96 registers a thread, and with shared memory
-// at its maximum a spilled register is a trip to L2.
+// CTA 0 for both).  In flight: two K tiles, three V tiles, two S and two P.
+// Four V tiles leave the loads in flight too little of L1 (2.59 ms for 2.29
+// then), two are too few for a tile's way of 6000 cycles (3.74 ms).  A second
+// softmax warpgroup left 96 registers a thread, and with shared memory at its
+// maximum a spilled register is a trip to L2.
+//
+// Measured: 4 x 512 new tokens x 64 heads behind up to 16384 FP8 entries 2.06
+// ms alone (1067 TFLOP/s), 2.30 ms back to back (956); 8 prompts of up to 2047
+// tokens x 32 heads 645 / 680 us (710 / 673 TFLOP/s); 4 x 1024 tokens, window
+// 128, 211 us (1.85 TB/s of queries, entries and output).  A tile of 128 x 64
+// takes about 2050 cycles: the tensor pipe is busy for half of them, shared
+// memory for two thirds, instruction issue for 57 %.
 #include "paged_attn.cuh"
 
 namespace csa {
@@ -823,8 +819,10 @@ __global__ void __launch_bounds__(128 * kPgCombRows) paged_attn_combine_kernel(c
 
 // Which kernel a call takes: the one-CTA kernel where the sequences have 64
 // rows or fewer on average, so that most items of 128 would be half empty.
-// 8 x 1 token x 64 heads behind up to 65536 FP8 entries: 118 us by pairs, 76
-// us by single CTAs; 4 x 512 tokens: 2.09 ms and CHUNK ms.
+// Pairs and single CTAs, back to back: 8 x 1 token x 64 heads behind up to
+// 65536 FP8 entries 119 and 94 us; 32 x 1 token x 16 heads, FP4, 106 and 70 us;
+// 16 x 1 token x 128 heads 117 and 144 us; 4 x 512 tokens x 64 heads 2.30 and
+// 3.42 ms.
 static bool pg_one(const csa_paged_attn_args* a) { return a->n_rows * a->H <= (int64_t)kPgRows / 2 * a->kv.B; }
 // Parts of the grid (pairs, or CTAs): all SMs, fewer when the call cannot have
 // two tiles for each.

@@ -13,11 +13,15 @@
 // S and the MN-major A operand of O^T, where the pair kernel's CTAs keep two
 // tiles and decode half of the other's channels as well.
 //
-// Bound: the tensor pipe and shared memory alike, about 1100 cycles a tile (S
-// 24 x 16 + 8 x 40, O^T 8 x 48; 32 KB written, 104 KB read).  Five tiles are in
-// flight, because a tile's way (decode, S, softmax, PV) is five times as long;
-// with tiles of 64 entries, two and a half of them, a tile took 3600 cycles
-// instead of twice PERIOD.
+// Bound: the tensor pipe and shared memory alike, about 1200 cycles a tile (S
+// 24 x 16 + 8 x 40, O^T 8 x 48; 36 KB written, 112 KB read); it takes 1250.
+// Five tiles are in flight, because a tile's way (decode, S, softmax, PV) is
+// five times as long; with tiles of 64 entries, two and a half of them, 64
+// entries took 3600 cycles.
+// Measured: 8 x 1 token x 64 heads behind up to 65536 FP8 entries 94 us (2.0
+// TB/s of entries, 500 TFLOP/s), of which 15 us are the first tile's way, the
+// last output and the combine; 32 x 1 token x 16 heads behind up to 16384 FP4
+// entries 70 us; one token behind 1000 entries 18 us.
 #include "paged_attn.cuh"
 
 namespace csa {
