@@ -96,19 +96,17 @@ CSA_DEV void pg_commit(uint64_t* bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
       ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
-template <bool ACC>
-CSA_DEV void pg_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+CSA_DEV void pg_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
       " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n}"
-      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "n"(ACC ? 1 : 0) : "memory");
+      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "r"(acc) : "memory");
 }
-template <bool ACC>
-CSA_DEV void pg_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc) {
+CSA_DEV void pg_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %4};\n"
       " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n}"
-      ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "n"(ACC ? 1 : 0) : "memory");
+      ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "r"(acc) : "memory");
 }
 CSA_DEV void pg_st32(void* p, const uint32_t* v) {   // 32 bytes, aligned
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
@@ -201,13 +199,18 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
           tc_fence_after();
           const uint32_t kd = kd0 + (t % kPgKBufs) * (kPgKBytes >> 4), sd = tbase + kPgSCol + 32 * si;
           if (pg_elect()) {
-            pg_mma_ts<false>(sd, tbase, kd, kPgIdescS);
+            // rolled by 64-channel blocks: unrolled, 5 KB of instructions
+            // missed the cache once a tile
+            uint32_t bd = kd;
+#pragma unroll 1
+            for (uint32_t kb = 0; kb < (uint32_t)kPgQTmemBlocks; ++kb, bd += kPgKBlk >> 4) {
 #pragma unroll
-            for (int ks = 1; ks < kD / 16; ++ks) {
-              const uint32_t kb = ks >> 2, sub = ks & 3;
-              const uint32_t bd = kd + kb * (kPgKBlk >> 4) + sub * 2;
-              if (kb < (uint32_t)kPgQTmemBlocks) pg_mma_ts<true>(sd, tbase + kb * 32 + sub * 8, bd, kPgIdescS);
-              else pg_mma_ss<true>(sd, qd + (kb - kPgQTmemBlocks) * (kPgQBlk >> 4) + sub * 2, bd, kPgIdescS);
+              for (uint32_t sub = 0; sub < 4; ++sub) pg_mma_ts(sd, tbase + kb * 32 + sub * 8, bd + sub * 2, kPgIdescS, kb | sub);
+            }
+#pragma unroll 1
+            for (uint32_t kb = 0; kb < 8u - kPgQTmemBlocks; ++kb, bd += kPgKBlk >> 4) {
+#pragma unroll
+              for (uint32_t sub = 0; sub < 4; ++sub) pg_mma_ss(sd, qd + kb * (kPgQBlk >> 4) + sub * 2, bd + sub * 2, kPgIdescS, 1);
             }
             pg_commit(s_full + si);
             pg_commit(k_free + t % kPgKBufs);
@@ -239,8 +242,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
               for (int ks = 0; ks < kPgE / 16; ++ks) {
                 const uint32_t bd = vd + 2 * nb * (kPgVBlk >> 4) + ks * (2048 >> 4), ad = pd + ks * 2;
-                if (ks == 0 && i == 0) pg_mma_ss<false>(tbase + kPgOCol + 128u * nb, ad, bd, kPgIdescO);
-                else pg_mma_ss<true>(tbase + kPgOCol + 128u * nb, ad, bd, kPgIdescO);
+                pg_mma_ss(tbase + kPgOCol + 128u * nb, ad, bd, kPgIdescO, ks | i);
               }
             }
             pg_commit(v_free + t % kPgVBufs);

@@ -71,29 +71,26 @@ CSA_DEV P1Smem carve_p1(uint8_t* p) {
   return s;
 }
 
-template <bool ACC>
-CSA_DEV void p1_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+CSA_DEV void p1_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %4};\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
-      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "n"(ACC ? 1 : 0) : "memory");
+      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "r"(acc) : "memory");
 }
-template <bool ACC>
-CSA_DEV void p1_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc) {
+CSA_DEV void p1_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %4};\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}"
-      ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "n"(ACC ? 1 : 0) : "memory");
+      ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "r"(acc) : "memory");
 }
 
 // P rows are 64 bytes (32 fp16): 64-byte swizzle for that operand.
 constexpr uint32_t kP1DescP = (512u >> 4) | 1u << 14 | 4u << 29;
-template <bool ACC>
-CSA_DEV void p1_mma_pv(uint32_t d, uint32_t v_lo, uint32_t p_lo, uint32_t idesc) {
+CSA_DEV void p1_mma_pv(uint32_t d, uint32_t v_lo, uint32_t p_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %4};\n mov.b64 b, {%2, %5};\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}"
-      ::"r"(d), "r"(v_lo), "r"(p_lo), "r"(idesc), "n"(kPgDesc), "n"(kP1DescP), "n"(ACC ? 1 : 0) : "memory");
+      ::"r"(d), "r"(v_lo), "r"(p_lo), "r"(idesc), "n"(kPgDesc), "n"(kP1DescP), "r"(acc) : "memory");
 }
 
 template <bool FP4>
@@ -162,13 +159,18 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
         tc_fence_after();
         const uint32_t kd = kd0 + bi * (kPgKBytes >> 4), sd = tbase + kPgSCol + kP1E * si;
         if (pg_elect()) {
-          p1_mma_ts<false>(sd, tbase, kd, idesc);
+          // rolled by 64-channel blocks: unrolled, 5 KB of instructions
+          // missed the cache once a tile
+          uint32_t bd = kd;
+#pragma unroll 1
+          for (uint32_t kb = 0; kb < (uint32_t)kPgQTmemBlocks; ++kb, bd += kPgKBlk >> 4) {
 #pragma unroll
-          for (int ks = 1; ks < kD / 16; ++ks) {
-            const uint32_t kb = ks >> 2, sub = ks & 3;
-            const uint32_t bd = kd + kb * (kPgKBlk >> 4) + sub * 2;
-            if (kb < (uint32_t)kPgQTmemBlocks) p1_mma_ts<true>(sd, tbase + kb * 32 + sub * 8, bd, idesc);
-            else p1_mma_ss<true>(sd, qd + (kb - kPgQTmemBlocks) * (kP1QBlk >> 4) + sub * 2, bd, idesc);
+            for (uint32_t sub = 0; sub < 4; ++sub) p1_mma_ts(sd, tbase + kb * 32 + sub * 8, bd + sub * 2, idesc, kb | sub);
+          }
+#pragma unroll 1
+          for (uint32_t kb = 0; kb < 8u - kPgQTmemBlocks; ++kb, bd += kPgKBlk >> 4) {
+#pragma unroll
+            for (uint32_t sub = 0; sub < 4; ++sub) p1_mma_ss(sd, qd + kb * (kP1QBlk >> 4) + sub * 2, bd + sub * 2, idesc, 1);
           }
           mma_commit(s_full + si);
         }
@@ -203,8 +205,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
 #pragma unroll
             for (int ks = 0; ks < kP1E / 16; ++ks) {
               const uint32_t ad = vd + 2 * c * (kPgKBlk >> 4) + ks * (2048 >> 4), bd = pd + ks * 2;
-              if (ks == 0 && i == 0) p1_mma_pv<false>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
-              else p1_mma_pv<true>(tbase + kPgOCol + 64u * c, ad, bd, idesc);
+              p1_mma_pv(tbase + kPgOCol + 64u * c, ad, bd, idesc, ks | i);
             }
           }
           mma_commit(kv_free + bi);
