@@ -35,8 +35,8 @@
 //
 // Measured: 4 x 512 new tokens x 64 heads behind up to 16384 FP8 entries 2.06
 // ms alone (1067 TFLOP/s), 2.30 ms back to back (956); 8 prompts of up to 2047
-// tokens x 32 heads 645 / 680 us (710 / 673 TFLOP/s); 4 x 1024 tokens, window
-// 128, 211 us (1.85 TB/s of queries, entries and output).  A tile of 128 x 64
+// tokens x 32 heads 645 / 678 us (710 / 675 TFLOP/s); 4 x 1024 tokens, window
+// 128, 206 us (1.89 TB/s of queries, entries and output).  A tile of 128 x 64
 // takes about 2050 cycles: the tensor pipe is busy for half of them, shared
 // memory for two thirds, instruction issue for 57 %.
 #include "paged_attn.cuh"
