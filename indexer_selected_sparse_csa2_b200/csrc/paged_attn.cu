@@ -51,7 +51,7 @@ constexpr int kPgVBlk = kPgE * 128;       // 64-channel block of a V tile
 constexpr int kPgVBytes = 4 * kPgVBlk;
 constexpr int kPgPBytes = kPgHalf * kPgE * 2;
 constexpr size_t kPgOperandBytes = 2 * kPgQBlk + kPgKBufs * kPgKBytes + kPgVBufs * kPgVBytes + 2 * kPgPBytes;
-constexpr size_t kPgSmemBytes = kPgOperandBytes + 3072;
+constexpr size_t kPgSmemBytes = kPgOperandBytes + 2048;   // and the small arrays
 static_assert(kPgSmemBytes <= 232448, "shared memory of a CTA");
 static_assert(kPgMaxB / 32 * 8 <= kPgVBufs * kPgVBytes, "the plan's group sums use the V tiles");
 

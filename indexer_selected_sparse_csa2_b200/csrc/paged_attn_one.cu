@@ -37,7 +37,7 @@ constexpr int kP1WarpS2 = kPgWarps;
 constexpr int kP1Bufs = 5;                // tiles in flight
 constexpr int kP1QBlk = 128 * 128;        // shared Q block: 128 rows x 64 fp16
 constexpr int kP1PBytes = kP1Rows * kP1E * 2;
-constexpr size_t kP1SmemBytes = 2 * kP1QBlk + kP1Bufs * (kPgKBytes + kP1PBytes) + 3072;
+constexpr size_t kP1SmemBytes = 2 * kP1QBlk + kP1Bufs * (kPgKBytes + kP1PBytes) + 2048;
 static_assert(kP1SmemBytes <= 232448, "shared memory of a CTA");
 static_assert(kPgMaxB / 32 * 8 <= kP1Bufs * kPgKBytes, "the plan's group sums use the entry tiles");
 
