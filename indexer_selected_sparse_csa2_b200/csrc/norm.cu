@@ -6,7 +6,8 @@
 // of squares and the output.  A thread owns C chunks of 8 neighbouring
 // channels, so a 32-channel scale block is 4 lanes and a 128-channel one 16
 // lanes of one warp, and their maxima meet by shuffles.
-//   dim <= 1024 : one warp per row (no shared memory, no barrier).
+//   dim <= 1024 : one warp per row (no shared memory, no barrier), 1 to 4 chunks
+//                 a lane (544 channels with 3 instead of 4: 27.1 -> 23.8 us).
 //   else        : one CTA of dim / (8 C) threads per row.
 // CTAs stay for several rows and load the next one before they reduce this
 // one, so that loads are in flight through the barrier and the stores (8192
@@ -197,8 +198,13 @@ static void launch_norm_src(const NormParams& p, cudaStream_t stream) {
     const int64_t rows_cta = 8;
     int64_t g = (p.n_rows + rows_cta - 1) / rows_cta;
     if (g > (int64_t)kNumSMs * 6) g = (int64_t)kNumSMs * 6;
-    if (chunks <= 64) launch_norm_t<SRC, 2, true>(p, 256, g, stream);
-    else launch_norm_t<SRC, 4, true>(p, 256, g, stream);
+    // as many chunks a lane as the row needs
+    switch ((chunks + 31) / 32) {
+      case 1: launch_norm_t<SRC, 1, true>(p, 256, g, stream); break;
+      case 2: launch_norm_t<SRC, 2, true>(p, 256, g, stream); break;
+      case 3: launch_norm_t<SRC, 3, true>(p, 256, g, stream); break;
+      default: launch_norm_t<SRC, 4, true>(p, 256, g, stream);
+    }
     return;
   }
   const int C = chunks <= 1024 ? 2 : 4;                     // dim <= 16384: at most 512 threads

@@ -102,6 +102,13 @@ def test_norm(csa, rows, dim, kind, dtype, residual):
         _check_codes(codes, scales, y, kind, "codes")
 
 
+@pytest.mark.parametrize("dim", [240, 256, 272, 528, 768, 784])
+def test_norm_around_the_chunks_of_a_lane(csa, dim):
+    """Rows where the number of 8-channel chunks a lane holds changes."""
+    for dtype in ("float32", "bfloat16"):
+        test_norm(csa, 70, dim, "plain", dtype, True)
+
+
 def test_norm_without_weight_and_with_zero_rows_of_channels(csa):
     x = torch.zeros(4, 256, device="cuda")
     x[1, 3] = 5.0
