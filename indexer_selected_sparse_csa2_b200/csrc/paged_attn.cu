@@ -38,7 +38,7 @@
 // tokens x 32 heads 645 / 678 us (710 / 675 TFLOP/s); 4 x 1024 tokens, window
 // 128, 206 us (1.89 TB/s of queries, entries and output).  A tile of 128 x 64
 // takes about 2050 cycles: the tensor pipe is busy for half of them, shared
-// memory for two thirds, instruction issue for 57 %.
+// memory for two thirds, instruction issue for 56 %.
 #include "paged_attn.cuh"
 
 namespace csa {
