@@ -330,12 +330,35 @@ def csa_sparse_attn(args: AttnArgs, workspace=None, stream=None, device=None) ->
     _check(_attn(ctypes.byref(args), _ptr(workspace), nbytes, _stream(stream)), "csa_sparse_attn")
 
 
+def _cuda_device(args, where: str):
+    """Device of the tensors that ``args`` was built from (None: the fields were
+    set by hand).  A kernel must not get host pointers: tensors elsewhere than
+    on a CUDA device are refused here, before any launch."""
+    dev = getattr(args, "_device", None)
+    if dev is not None and dev.type != "cuda":
+        raise ValueError(f"{where}: tensors must be on a CUDA device, not on {dev}")
+    return dev
+
+
+def _workspace_bytes(workspace, dev, where: str) -> int:
+    """Size of a workspace tensor; ``dev``: the device it has to be on (None: any
+    CUDA device).  A view with gaps or repeats spans other bytes than its
+    elements' sum."""
+    if workspace is None:
+        return 0
+    if not workspace.is_cuda or (dev is not None and workspace.device != dev):
+        raise ValueError(f"{where}: workspace is on {workspace.device}, not on {dev or 'a CUDA device'}")
+    if not workspace.is_contiguous():
+        raise ValueError(f"{where}: workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
 def _on_device(args, stream, call, where: str) -> None:
     """call(raw stream) on the device of the arguments' tensors, which need not
     be the current one; ``stream`` None = that device's current stream."""
+    dev = _cuda_device(args, where)
     cuda = _torch().cuda
-    dev = getattr(args, "_device", None)
-    if dev is None or dev == cuda.current_device():
+    if dev is None or dev.index == cuda.current_device():
         _check(call(_stream(stream)), where)
         return
     with cuda.device(dev):
@@ -355,13 +378,12 @@ def csa_paged_attn_workspace_size(args: PagedAttnArgs) -> int:
 
 
 def csa_paged_attn(args: PagedAttnArgs, workspace=None, stream=None, device=None) -> None:
+    dev = _cuda_device(args, "csa_paged_attn")
     # the library checks a given workspace's size itself; query it only to allocate one
     if workspace is None:
-        dev = getattr(args, "_device", None)
-        where = device or ("cuda" if dev is None else f"cuda:{dev}")
         with _torch().cuda.stream(stream):          # its memory is the stream's: freed here, reused behind the call
-            workspace = _workspace(csa_paged_attn_workspace_size(args), where)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+            workspace = _workspace(csa_paged_attn_workspace_size(args), device or dev or "cuda")
+    nbytes = _workspace_bytes(workspace, dev, "csa_paged_attn")
     _on_device(args, stream, lambda st: _paged_attn(args, _ptr(workspace), nbytes, st), "csa_paged_attn")
 
 
@@ -545,11 +567,11 @@ def _expect(t, dtype: str, what: str, shape=None, contiguous=False) -> None:
 
 
 def _device_of(*tensors):
-    """Index of the CUDA device that all of the tensors are on (None: the CPU)."""
+    """The device that all of the tensors are on."""
     devs = {t.device for t in tensors if t is not None}
     if len(devs) != 1:
         raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return devs.pop().index
+    return devs.pop()
 
 
 def _row_stride(t) -> int:

@@ -237,3 +237,52 @@ def test_argument_builders_check_types_and_shapes(csa):
     # one row, whatever stride a one-row view carries
     one = csa.rms_norm_args(x=z(64, 3).t()[:1].contiguous(), out=z(1, 64))
     assert one.x_stride >= 64 and one.out_stride >= 64
+
+
+def test_calls_refuse_host_tensors(csa):
+    """The builders take CPU tensors; the calls must not hand their addresses to
+    a kernel."""
+    z = torch.zeros
+    kv = csa.paged_kv(pages=z(3, 16, 528, dtype=torch.uint8), block_table=z(2, 3, dtype=torch.int32),
+                      cu_q=z(3, dtype=torch.int32), kv_len=z(2, dtype=torch.int32))
+    q = z(4, 16, 512, dtype=torch.bfloat16)
+    attn = csa.paged_attn_args(q=q, kv=kv, out=torch.empty_like(q), softmax_scale=1.0)
+    for call, args in ((csa.csa_rms_norm, csa.rms_norm_args(x=z(2, 64), out=z(2, 64))),
+                       (csa.csa_paged_append, csa.paged_append_args(src=z(4, 512), kv=kv)),
+                       (csa.csa_paged_attn, attn)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(args)
+    with pytest.raises(ValueError, match="CUDA device"):
+        csa.csa_paged_attn(attn, workspace=z(1 << 20, dtype=torch.uint8))
+
+
+def test_attention_refuses_workspaces_it_could_not_write(csa):
+    """On the host, on another device than the arguments, and views whose
+    element count is not the size of their memory."""
+    kv = csa.PagedAttnArgs()
+    _kv(csa, kv.kv)
+    kv.q = kv.out = 4096
+    kv.n_rows, kv.H, kv.D, kv.q_row_stride, kv.q_head_stride, kv.softmax_scale = 5, 16, 512, 16 * 512, 512, 0.05
+    need = csa.csa_paged_attn_workspace_size(kv)
+    with pytest.raises(ValueError, match="workspace"):
+        csa.csa_paged_attn(kv, workspace=torch.zeros(need, dtype=torch.uint8))
+
+    class Workspace:                                  # stands in for a tensor on a GPU
+        is_cuda, device = True, torch.device("cuda", 1)
+
+        def __init__(self, contiguous):
+            self.is_contiguous = lambda: contiguous
+
+        def numel(self):
+            return need
+
+        def element_size(self):
+            return 1
+
+    for dev in (None, torch.device("cuda", 1)):
+        assert csa._workspace_bytes(Workspace(True), dev, "call") == need
+        with pytest.raises(ValueError, match="contiguous"):
+            csa._workspace_bytes(Workspace(False), dev, "call")
+    with pytest.raises(ValueError, match="cuda:0"):
+        csa._workspace_bytes(Workspace(True), torch.device("cuda", 0), "call")
+    assert csa._workspace_bytes(None, None, "call") == 0
