@@ -358,7 +358,9 @@ csa_status csa_paged_append(const csa_paged_append_args* a, csa_stream_t stream)
  * that does not (NaN codes, a scale past the range) may spoil any row of its
  * sequence in the call, also one whose mask leaves it out; entries that no row
  * of the call sees are not looked at, whatever their bytes.  A query that does
- * not spoils its own row.
+ * not spoils its own row, and so does a logit that fp32 cannot hold: |l_e| must
+ * stay below 2.3e38 (fp32's largest value / log2 e), as it does with any such
+ * operands up to softmax_scale = 1e26.
  * The workspace holds partial results from the call to its end: calls that may
  * run at the same time (two streams, two captured graphs) need one each. */
 typedef struct {

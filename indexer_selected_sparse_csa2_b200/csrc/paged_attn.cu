@@ -511,9 +511,6 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     const int q4 = warp, rr = 32 * (q4 & 1) + lane;          // TMEM lane quarter, row of this CTA
     const int half = q4 >> 1;                                // entries 32 half .. of a tile; channel half of a block
     const uint32_t trow = tbase + ((uint32_t)(32 * q4) << 16);
-    // scale 0: logits 0 with factor 1, since -inf * 0 is not a number
-    const bool zero = p.scale_log2 == 0.f;
-    const float sc = zero ? 1.f : p.scale_log2;
     const uint32_t s_free_at = dsmem(s_free, 0), p_full_at = dsmem(p_full, 0);
     PgWalk<kPgRows> w;
     uint32_t t = 0, seg = 0;
@@ -547,10 +544,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         tc_fence_before();
         __syncwarp();
         if (lane == 0) pg_arrive(s_free_at + 8 * si);
-        if (zero) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) sv[k] = 0u;
-        }
+        // rounded before anything is subtracted (pg_mul32)
+        pg_mul32(sv, p.scale_log2);
         if (!__all_sync(0xffffffffu, mask == 0xffffffffu)) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) sv[k] = ((mask >> k) & 1u) ? sv[k] : 0xff800000u;   // -inf
@@ -560,17 +555,16 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         for (int k = 0; k < 4; ++k) m4[k] = fmaxf(__uint_as_float(sv[k]), __uint_as_float(sv[k + 4]));
 #pragma unroll
         for (int k = 8; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(sv[k]));
-        float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        if (mt != -INFINITY) mt *= sc;
+        const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         S.mx[(2 * si + half) * 64 + rr] = mt;
         uint32_t over;
         // a row's two halves are lanes of warps w and w + 2: they meet here
         asm volatile("{\n .reg .pred q, r;\n setp.ne.u32 q, %2, 0;\n bar.red.or.pred r, %1, 64, q;\n selp.u32 %0, 1, 0, r;\n}"
-                     : "=r"(over) : "r"(1 + (q4 & 1)), "r"(mt > m_run + kPgRescale ? 1u : 0u) : "memory");
+                     : "=r"(over) : "r"(1 + (q4 & 1)), "r"(mt - m_run >= kPgRescale ? 1u : 0u) : "memory");
         if (over) {
           const float mm = fmaxf(mt, S.mx[(2 * si + (half ^ 1)) * 64 + rr]);
           float alpha = 1.f;
-          if (mm > m_run + kPgRescale) {
+          if (mm - m_run >= kPgRescale) {
             alpha = m_run == -INFINITY ? 0.f : pg_ex2(m_run - mm);
             m_run = mm;
             l_run *= alpha;
@@ -598,7 +592,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
         if (t >= 2) ok = ok && pg_wait_warp(v_free + (t - 2) % kPgVBufs, ((t - 2) / kPgVBufs) & 1u, kErrWaitSmemEmpty);
         // a row that has seen nothing yet: every logit here is -inf, and so is
         // its max; any finite reference gives the zeros it needs
-        const float mref = m_run == -INFINITY ? 0.f : m_run - kPgPExp;
+        pg_add32(sv, m_run == -INFINITY ? 0.f : kPgPExp - m_run);
         float l0 = 0.f, l1 = 0.f;
         uint8_t* pt = S.p + si * kPgPBytes;
 #pragma unroll
@@ -607,8 +601,8 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int e0 = 8 * c + 2 * k;
-            const float x0 = pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref));
-            const float x1 = pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref));
+            const float x0 = pg_ex2(__uint_as_float(sv[e0]));
+            const float x1 = pg_ex2(__uint_as_float(sv[e0 + 1]));
             l0 += x0;
             l1 += x1;
             o[k] = pg_h2u(__floats2half2_rn(x0, x1));

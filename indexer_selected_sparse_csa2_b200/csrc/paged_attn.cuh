@@ -15,9 +15,11 @@
 // timing.
 //
 // Online softmax in the exp2 domain; the running max moves only when a tile's
-// max exceeds it by more than kPgRescale, and only then O is rescaled in TMEM.
+// max exceeds it by kPgRescale or more, and only then O is rescaled in TMEM.
 // P is held in fp16 times 2^6: at most 2^14, and weights down to 2^-31 of the
-// max keep a value.
+// max keep a value.  (Past 2^24 fp32 values are 2 and more apart, and 6 - max
+// may round up to 8 - max: with less than kPgRescale between a logit and the
+// running max that still stays below 2^13.)
 #pragma once
 #include <climits>
 
@@ -91,6 +93,24 @@ CSA_DEV float pg_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 32 logits times the scale, and minus the max, two an instruction (one fma for
+// both would need as many).  The product is rounded before the difference is
+// taken: a max is a rounded product too, and where logits pass 2^24 an fma's
+// exact product may lie whole units from it, so that the largest weight left
+// fp16's range or vanished.
+CSA_DEV void pg_mul32(uint32_t (&s)[32], float f) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2)
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mul.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "+r"(s[k]), "+r"(s[k + 1]) : "f"(f));
+}
+CSA_DEV void pg_add32(uint32_t (&s)[32], float f) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 2)
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}"
+        : "+r"(s[k]), "+r"(s[k + 1]) : "f"(f));
 }
 
 // Bounded wait by a whole warp, the same answer in every lane.

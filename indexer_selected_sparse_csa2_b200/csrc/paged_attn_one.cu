@@ -379,9 +379,6 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
     const int rr = 32 * (warp & 1) + lane;     // row of the item
     const uint32_t grp = (uint32_t)warp >> 1;
     const uint32_t trow = tbase + ((uint32_t)(32 * warp) << 16);
-    // scale 0: logits 0 with factor 1, since -inf * 0 is not a number
-    const bool zero = p.scale_log2 == 0.f;
-    const float sc = zero ? 1.f : p.scale_log2;
     PgWalk<kP1Rows> w;
     uint32_t t = 0, seg = 0;
     bool ok = true;
@@ -418,10 +415,8 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free + si);
-          if (zero) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) sv[k] = 0u;
-          }
+          // rounded before anything is subtracted (pg_mul32)
+          pg_mul32(sv, p.scale_log2);
           if (!__all_sync(0xffffffffu, mask == 0xffffffffu)) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) sv[k] = ((mask >> k) & 1u) ? sv[k] : 0xff800000u;   // -inf
@@ -432,16 +427,15 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
 #pragma unroll
           for (int k = 8; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(sv[k]));
           mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          if (mt != -INFINITY) mt *= sc;
           S.mx[64 * si + rr] = mt;
         }
         uint32_t over;
         asm volatile("{\n .reg .pred q, r;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred r, 1, 128, q;\n selp.u32 %0, 1, 0, r;\n}"
-                     : "=r"(over) : "r"(mt > m_run + kPgRescale ? 1u : 0u) : "memory");
+                     : "=r"(over) : "r"(mt - m_run >= kPgRescale ? 1u : 0u) : "memory");
         if (over) {
           const float mm = S.mx[64 * si + rr];
           float alpha = 1.f;
-          if (mm > m_run + kPgRescale) {
+          if (mm - m_run >= kPgRescale) {
             alpha = m_run == -INFINITY ? 0.f : pg_ex2(m_run - mm);
             m_run = mm;
             l_run *= alpha;
@@ -479,7 +473,7 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
           // PV that read both last.  A row that has seen nothing yet: every
           // logit here is -inf, and so is its max; any finite reference gives
           // the zeros it needs
-          const float mref = m_run == -INFINITY ? 0.f : m_run - kPgPExp;
+          pg_add32(sv, m_run == -INFINITY ? 0.f : kPgPExp - m_run);
           float l0 = 0.f, l1 = 0.f;
           uint8_t* pt = S.p + bi * kP1PBytes;
 #pragma unroll
@@ -488,8 +482,8 @@ __global__ void __launch_bounds__(kP1Threads, 1) paged_attn_one_kernel(const __g
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int e0 = 8 * c + 2 * k;
-              const float x0 = pg_ex2(fmaf(__uint_as_float(sv[e0]), sc, -mref));
-              const float x1 = pg_ex2(fmaf(__uint_as_float(sv[e0 + 1]), sc, -mref));
+              const float x0 = pg_ex2(__uint_as_float(sv[e0]));
+              const float x1 = pg_ex2(__uint_as_float(sv[e0 + 1]));
               l0 += x0;
               l1 += x1;
               o[k] = pg_h2u(__floats2half2_rn(x0, x1));

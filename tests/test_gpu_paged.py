@@ -514,6 +514,97 @@ def test_more_than_a_thousand_sequences(csa, H):
     _check(out, lse, B.want(sink=B.sink))
 
 
+def _check_far_logits(B, out, lse, scale, sink=None):
+    """Logits so large that their own error is many units (2^-18 of the sum of
+    magnitudes, plus 2^-22 of the logit for its scaling).  A row whose largest
+    logit leads the others by 40 beyond both errors takes that entry alone: the
+    others' weights are below e^-40, so out is x_e within the weight's and the
+    output's rounding, 2^-11 + 2^-8, and e^-40 of the sum of magnitudes; lse is
+    the logit within its error.  The other rows are finite, and no larger than
+    the largest entry.  A sink is one more logit whose entry is zero.  Returns
+    the number of rows with such a leader."""
+    led = 0
+    g, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    q, sc = B.q.double().numpy(), float(np.float32(scale))
+    for r, (b, p) in enumerate(row_positions(B.cu, B.kv)):
+        kp, X = gather(B.pages, B.table, b, range(0, p + 1))
+        X = np.concatenate([X, np.zeros((1, 512))])                 # the sink's
+        logit = sc * (q[r] @ X.T)
+        err = 2.0 ** -18 * sc * (np.abs(q[r]) @ np.abs(X).T) + 2.0 ** -22 * np.abs(logit)
+        logit[:, -1] = -np.inf if sink is None else sink
+        assert np.all(np.isfinite(g[r])) and np.all(np.isfinite(gl[r])), (r, p)
+        size = np.abs(X).max(0)
+        assert np.all(np.abs(g[r]) <= size * (1 + 2.0 ** -7)), (r, p)
+        for h in range(B.H):
+            e = int(np.argmax(logit[h]))
+            rest = np.delete(logit[h] + err[h], e)
+            if len(rest) and logit[h, e] - err[h, e] - rest.max() < 40:
+                continue
+            led += 1
+            tol = (2.0 ** -8 + 2.0 ** -11) * np.abs(X[e]) + np.exp(-40.0) * np.abs(X).sum(0)
+            assert np.all(np.abs(g[r, h] - X[e]) <= tol), (r, p, h)
+            assert abs(gl[r, h] - logit[h, e]) <= err[h, e] + 2.0 ** -20 * (1 + abs(logit[h, e])), (r, p, h)
+    return led
+
+
+def _set_entries(B, b, x):
+    e = _encode(x.astype(np.float32), B.fmt)
+    for p in range(0, len(e), B.page):
+        k = min(B.page, len(e) - p)
+        B.pages[B.table[b, p // B.page], :k] = e[p:p + k]
+
+
+FAR = [(2.0, 1.0, 2.0 ** 20), (2.0, 1.0, 2.0 ** 23), (2.0, 1.0, 1e12), (2.0, 1.0, 1e26), ("most", "most", 1e26)]
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("case", range(len(FAR)))
+def test_logits_far_past_fp32_integers(csa, case, fmt, few):
+    """Logits up to the largest that fp32 holds (times log2 e), with maxima that
+    grow along the cache: in base 2 they are past 2^24, where neighbouring fp32
+    values are whole units apart."""
+    gain, spread, scale = FAR[case]
+    lens = [(4, 900), (2, 130), (3, 3)]
+    H = 16 if few else 32
+    B = Batch(400 + case, _thin(lens, H) if few else lens, H, fmt, 16)
+    rng = np.random.default_rng(500 + case)
+    top = 6e4 if fmt == "fp8" else 2600.0                  # an FP4 entry decodes to at most 2688
+    if gain == "most":
+        q = np.clip(rng.standard_normal(B.q.shape) * 2e4, -65024, 65024)
+        q[3, 0] = 65024 * np.where(rng.random(512) < 0.5, -1, 1)
+        B.q = torch.from_numpy(q.astype(np.float32)).to(torch.bfloat16)
+    for b, (n, T) in enumerate(lens):
+        if gain == "most":
+            x = np.clip(rng.standard_normal((T, 512)) * top / 4, -top, top)
+            if b == 0:                                     # the largest products there are, of either sign
+                x[333], x[777] = -top * np.sign(q[3, 0]), top * np.sign(q[3, 0])
+        else:
+            x = rng.standard_normal((T, 512)) * np.linspace(0.05, 6.0, T)[:, None]
+        _set_entries(B, b, x)
+    kv = B.device(csa)
+    for sink in (None, B.sink):
+        out, lse = _run(csa, B, kv, sink=sink, scale=scale)
+        assert _check_far_logits(B, out, lse, scale, sink) > 9 * H // 2
+
+
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("scale", [2.0 ** 20, 1e9, 1e26])
+def test_far_logits_that_are_all_the_same(csa, few, scale):
+    """Every entry of the cache alike: any weights give that entry."""
+    B = Batch(410, _thin([(3, 500)], 32) if few else [(3, 500)], 32, "fp8", 16)
+    x = np.random.default_rng(9).standard_normal((1, 512))
+    _set_entries(B, 0, np.repeat(x, 500, 0))
+    out, lse = _run(csa, B, B.device(csa), scale=scale)
+    _, X = gather(B.pages, B.table, 0, range(1))
+    logit = float(np.float32(scale)) * (B.q.double().numpy() @ X[0])
+    size = float(np.float32(scale)) * (np.abs(B.q.double().numpy()) @ np.abs(X[0]))
+    # the weights' rounding is the same for all: at most 2^-11, and 2^-8 of the output's
+    assert np.all(np.abs(out.double().cpu().numpy() - X[0]) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(X[0]))
+    n = np.array([498, 499, 500])[:, None]
+    assert np.all(np.abs(lse.double().cpu().numpy() - logit - np.log(n)) <= 2.0 ** -18 * size + 2.0 ** -20 * (1 + np.abs(logit)))
+
+
 # -------------------------------------------------------------------- append
 def _append(csa, B, src, n_rows=None, **kw):
     kv = B.device(csa)
