@@ -66,6 +66,7 @@ struct PgSmem {
   int64_t* start;    // the pair's range: {its start inside its first item, length, sequence, item, PgSeq}
   uint64_t* bars;
   uint32_t* tmem_base;
+  volatile uint32_t* begun;   // items with tiles whose queries the decode warps have turned to
 };
 
 CSA_DEV PgSmem carve_pg(uint8_t* p) {
@@ -79,7 +80,8 @@ CSA_DEV PgSmem carve_pg(uint8_t* p) {
   s.bars = reinterpret_cast<uint64_t*>(p); p += 24 * 8;
   s.start = reinterpret_cast<int64_t*>(p); p += 8 * 8;
   s.valid = reinterpret_cast<uint32_t*>(p); p += 2 * kPgVBufs * 4;
-  s.tmem_base = reinterpret_cast<uint32_t*>(p);
+  s.tmem_base = reinterpret_cast<uint32_t*>(p); p += 4;
+  s.begun = reinterpret_cast<uint32_t*>(p);
   return s;
 }
 
@@ -168,6 +170,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
     mbar_init(q_free, 1);
     mbar_init(acc_done, 1);
     fence_mbar_init();
+    *S.begun = 1;
   }
   if (warp == kPgWarpS) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(S.tmem_base)), "r"(kPgTmemCols)
@@ -254,15 +257,18 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       if (pg_elect()) pg_commit(drain + 1);
       __syncwarp();
     } else {
-      // CTA 1's warp fetches the next item's query rows, of both CTAs, into L2
-      // once an item's last S is done
+      // CTA 1's warp fetches an item's query rows, of both CTAs, into L2 once
+      // the decode warps have turned to the item before.  It follows a count,
+      // not a barrier's phase: nobody waits for this warp, so it may fall any
+      // number of items behind; and a wait that gives up (an item may take as
+      // long) ends the prefetching, not the result.
       PgWalk<kPgRows> w;
-      uint32_t seg = 0;
+      uint32_t items = 0;                // with tiles, up to this one
       bool ok = true;
-      for (bool go = w.begin(p, S.start); go && ok;) {
-        const bool tiles = w.take > 0;
-        go = w.next(p);
-        if (go && w.take > 0) {
+      for (bool go = w.begin(p, S.start); go && ok; go = w.next(p)) {
+        if (w.take == 0) continue;
+        if (items > 0) ok = pg_wait_count(S.begun, items);
+        if (items++ > 0 && ok) {
           const int n = min(w.s.n * a.H - w.j * kPgRows, kPgRows);
           for (int l = lane; l < 8 * n; l += 32) {         // 128 bytes each
             int head;
@@ -272,7 +278,6 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
             asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
           }
         }
-        if (go && tiles) ok = pg_wait_warp(q_free, seg++ & 1u, kErrWaitSmemEmpty);
       }
     }
   } else if (warp >= kPgWarpDec) {
@@ -393,6 +398,7 @@ __global__ void __launch_bounds__(kPgThreads, 1) paged_attn_kernel(const __grid_
       const PgRowsIn R = rows();
       if (seg > 0) {
         ok = ok && pg_wait_warp(q_free, (seg - 1) & 1u, kErrWaitSmemEmpty);
+        if (tid == 32 * kPgWarpDec) *S.begun = seg + 1;
         if (ok) pg_fetch_q(p, R, q_buf, wq, lane, g);
       }
       tc_fence_after();

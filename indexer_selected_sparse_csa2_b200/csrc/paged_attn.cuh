@@ -117,6 +117,16 @@ CSA_DEV void pg_add32(uint32_t (&s)[32], float f) {
 CSA_DEV bool pg_wait_warp(uint64_t* bar, uint32_t parity, int code) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, &g_pg_error, code));
 }
+// Bounded wait by a whole warp for a count in shared memory; giving up is no error.
+CSA_DEV bool pg_wait_count(const volatile uint32_t* count, uint32_t n) {
+  const uint64_t t0 = global_ns();
+  bool there = *count >= n;
+  while (!there && global_ns() - t0 <= kWaitNs) {
+    __nanosleep(200);
+    there = *count >= n;
+  }
+  return __all_sync(0xffffffffu, there);
+}
 // MMAs with descriptors given by their low words (the high word is a constant
 // of the layout: 128-byte swizzle, 8-row groups 1024 bytes apart), so that an
 // unrolled sequence costs one addition per operand; issued by one lane of a

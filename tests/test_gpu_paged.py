@@ -605,6 +605,30 @@ def test_far_logits_that_are_all_the_same(csa, few, scale):
     assert np.all(np.abs(lse.double().cpu().numpy() - logit - np.log(n)) <= 2.0 ** -18 * size + 2.0 ** -20 * (1 + np.abs(logit)))
 
 
+def test_thousands_of_items_of_one_tile_and_of_none(csa):
+    """A window of one entry: items as short as they get, over which every warp
+    has to keep up or not matter, with items between them that see nothing.  A
+    row's output is its own entry (weight 1: rounded by 2^-11 and 2^-8)."""
+    B = Batch(31, [(900, 900), (600, 200), (5, 5), (700, 3000)], 128, "fp8", 16)
+    q = B.q.cuda()
+    for _ in range(3):
+        out, lse = _run(csa, B, B.device(csa), window=1, q=q)
+    X, seen = torch.zeros(B.rows, 512), np.zeros(B.rows, dtype=bool)
+    for r, (b, p) in enumerate(row_positions(B.cu, B.kv)):
+        if p >= 0:
+            X[r] = torch.from_numpy(gather(B.pages, B.table, b, [p])[1][0])       # E4M3 times a power of two: exact
+            seen[r] = True
+    X = X.cuda()
+    for i in range(0, B.rows, 256):
+        x = X[i:i + 256].double()[:, None]
+        assert bool(((out[i:i + 256].double() - x).abs() <= (2.0 ** -8 + 2.0 ** -11) * x.abs()).all())
+        z = q[i:i + 256].double() * x
+        want, size = 512 ** -0.5 * z.sum(-1), 512 ** -0.5 * z.abs().sum(-1)
+        on = torch.from_numpy(seen[i:i + 256]).cuda()
+        assert bool((((lse[i:i + 256].double() - want).abs() <= 2.0 ** -17 * size + 2.0 ** -18 * (1 + want.abs()))[on]).all())
+        assert bool(torch.isneginf(lse[i:i + 256][~on]).all())
+
+
 # -------------------------------------------------------------------- append
 def _append(csa, B, src, n_rows=None, **kw):
     kv = B.device(csa)
