@@ -110,10 +110,6 @@ CSA_DEV void pg_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t ides
       " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n}"
       ::"r"(d), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kPgDesc), "r"(acc) : "memory");
 }
-CSA_DEV void pg_st32(void* p, const uint32_t* v) {   // 32 bytes, aligned
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
-}
 // Instruction descriptor with B MN-major (bit 16).
 constexpr uint32_t kPgIdescS = (1u << 4) | ((uint32_t)(kPgE >> 3) << 17) | ((uint32_t)(kPgRows >> 4) << 24);
 constexpr uint32_t kPgIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(256 >> 3) << 17) | ((uint32_t)(kPgRows >> 4) << 24);

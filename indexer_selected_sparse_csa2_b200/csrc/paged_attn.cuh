@@ -88,7 +88,6 @@ CSA_DEV uint4 pg_ld_entry(const void* p) {
   return r;
 }
 CSA_DEV uint32_t pg_h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-CSA_DEV __half2 pg_u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 CSA_DEV float pg_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
