@@ -177,3 +177,24 @@ def test_norm_same_bits_whatever_the_other_rows(csa):
     for i in (0, 1, 500, 899):
         for a, b in zip(whole, go(x[i:i + 1], r[i:i + 1])):
             assert torch.equal(a[i:i + 1], b)
+
+
+@pytest.mark.parametrize("rows,dim,kind", [(7105, 512, "ue8m0"), (7300, 16, "plain"), (14300, 544, "ue8m0"), (9001, 1024, "f32")])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_norm_of_more_rows_than_warps(csa, rows, dim, kind, dtype):
+    """Short rows from the 7105th on are a warp's second and third ones."""
+    test_norm(csa, rows, dim, kind, dtype, True)
+
+
+@pytest.mark.parametrize("rows,dim", [(7400, 256), (15000, 640), (3000, 2048)])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_norm_in_place_where_rows_are_loaded_ahead(csa, rows, dim, dtype):
+    """Both outputs over both inputs, bit for bit the separate ones: a row's
+    loads go out before the row before it is written."""
+    dt = getattr(torch, dtype)
+    x, r, w = _inputs(rows, rows, dim, dt)
+    out, ro = torch.empty_like(x), torch.empty_like(x)
+    csa.csa_rms_norm(csa.rms_norm_args(x=x, residual=r, residual_out=ro, weight=w, out=out))
+    csa.csa_rms_norm(csa.rms_norm_args(x=x, residual=r, residual_out=r, weight=w, out=x))
+    torch.cuda.synchronize()
+    assert torch.equal(x, out) and torch.equal(r, ro)

@@ -707,6 +707,107 @@ def test_append_skips_what_has_no_entry(csa):
     assert np.array_equal(_append(csa, B, x), want)
 
 
+class Rows:
+    """Packed rows for an append of thousands: a cache of random bytes, a table
+    with holes, sequences of the given (new tokens, length), padding rows."""
+
+    def __init__(self, seed, lens, fmt, page, dtype):
+        rng = np.random.default_rng(seed)
+        self.lens, self.fmt, self.page = lens, fmt, page
+        need = [max(0, -(-T // page)) for _, T in lens]
+        self.n_pages = sum(need) + 1
+        ids = rng.permutation(self.n_pages).astype(np.int32)
+        table = np.full((len(lens), max(need) + 1), -1, dtype=np.int32)
+        for b, k in enumerate(need):
+            table[b, :k] = ids[sum(need[:b]):sum(need[:b]) + k]
+        holes = rng.random(table.shape) < 0.02
+        self.table = np.where(holes, rng.choice([-1, self.n_pages, 2 ** 31 - 1], table.shape), table).astype(np.int32)
+        self.cu = np.concatenate([[0], np.cumsum([n for n, _ in lens])]).astype(np.int32)
+        self.kv = np.array([T for _, T in lens], dtype=np.int32)
+        self.n = int(self.cu[-1])
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.src = (torch.randn(self.n + 5, 512, generator=g, device="cuda") * 3).to(dtype)
+        self.weight = 1 + 0.2 * torch.randn(512, generator=g, device="cuda")
+        angle = 6.3 * torch.rand(self.n + 5, 32, generator=g, device="cuda")
+        self.cs = torch.stack([angle.cos(), angle.sin()], -1)
+        self.pages = torch.randint(0, 256, (self.n_pages, page, ENTRY[fmt]), generator=g, device="cuda", dtype=torch.uint8)
+
+    def places(self):
+        """Entry number of every row (-1: none), by sequence."""
+        at = np.full(self.n, -1, dtype=np.int64)
+        for b, (n, T) in enumerate(self.lens):
+            p = np.arange(T - n, T)
+            pg = np.where(p >= 0, p // self.page, -1)
+            on = (pg >= 0) & (pg < self.table.shape[1])
+            g = np.where(on, self.table[b, np.where(on, pg, 0)], -1)
+            on &= (g >= 0) & (g < self.n_pages)
+            at[self.cu[b]:self.cu[b + 1]] = np.where(on, g.astype(np.int64) * self.page + p % self.page, -1)
+        return at
+
+    def append(self, csa, i=0, j=None, **kw):
+        """Rows [i, j) (None: all, and the padding) appended to a copy of the
+        cache, or to `into`."""
+        pages = kw.pop("into", None)
+        pages = self.pages.clone() if pages is None else pages
+        e = self.n if j is None else j
+        cu = np.clip(self.cu, i, e) - i
+        kv_len = self.kv - (self.cu[1:] - np.clip(self.cu[1:], i, e))
+        dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()  # noqa: E731
+        kv = csa.paged_kv(pages=pages, block_table=dev(self.table), cu_q=dev(cu), kv_len=dev(kv_len))
+        src = self.src[i:] if j is None else self.src[i:j]
+        rope = self.cs[i:] if j is None else self.cs[i:j]
+        csa.csa_paged_append(csa.paged_append_args(src=src, kv=kv, rope_cs=rope if kw.pop("rope", False) else None, **kw))
+        torch.cuda.synchronize()
+        return pages
+
+
+_R = np.random.default_rng(77)
+MANY = [  # from 2369 rows on a warp takes several neighbouring ones: 2, 3, 4 and 32 here, the last in several goes
+    ([(2000, 2500), (0, 40), (369, 369)], 16),
+    ([(1, 1)] * 20 + [(2400, 2300)] + [(0, 9)] * 5 + [(2583, 9000)], 33),
+    ([(int(n), int(n) + int(t)) for n, t in zip(_R.integers(0, 250, 75), _R.integers(-20, 300, 75))], 7),
+    ([(40000, 40000), (0, 1), (36011, 36100), (3, 3)], 64),
+    ([(int(n), int(n)) for n in _R.integers(0, 2100, 80)], 16),
+]
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_append_of_thousands_of_rows(csa, fmt, dtype, case):
+    """Entries bit for bit csa_quant_kv's, and with norm and rotation those of
+    the same rows appended 1000 at a time (a warp a row); what has no entry, and
+    every other byte of the cache, stays."""
+    lens, page = MANY[case]
+    R = Rows(600 + case, lens, fmt, page, getattr(torch, dtype))
+    assert R.n > 2368
+    at = torch.from_numpy(R.places()).cuda()
+    on = at >= 0
+    assert bool(on.any()) and not bool(on.all())
+    enc = torch.empty(R.n, ENTRY[fmt], dtype=torch.uint8, device="cuda")
+    csa.csa_quant_kv(R.src[:R.n], csa.CSA_FMT_FP8_E4M3_UE8M0X32 if fmt == "fp8" else csa.CSA_FMT_FP4_E2M1_E4M3X16, enc)
+    pick = np.random.default_rng(case).integers(0, R.n, 50)
+    assert np.array_equal(enc[pick].cpu().numpy(), _encode(R.src[pick].float().cpu().numpy(), fmt))
+    want = R.pages.clone()
+    want.view(-1, ENTRY[fmt])[at[on]] = enc[on]
+    assert torch.equal(R.append(csa), want)
+    kw = dict(norm=True, weight=R.weight, eps=1e-5, rope=True)
+    parts = R.pages.clone()
+    for i in range(0, R.n, 1000):
+        R.append(csa, i, min(i + 1000, R.n), into=parts, **kw)
+    whole = R.append(csa, **kw)
+    assert torch.equal(whole, parts)
+    # those are the normed and rotated rows: a sample against float64, as above
+    if fmt == "fp8":
+        rows = pick[on[pick].cpu().numpy()]
+        _, y = rms_norm(R.src[rows].double().cpu().numpy(), 1e-5, R.weight.double().cpu().numpy())
+        y = np.concatenate([orope.rotate(y[i:i + 1], R.cs[r].cpu().numpy()) for i, r in enumerate(rows)])
+        raw = whole.view(-1, 528)[at[rows]].cpu().numpy()
+        s = np.repeat(np.ldexp(1.0, raw[:, 512:].astype(int) - 127), 32, axis=1)
+        err = np.abs(fp8_window_dequant_rows(raw) - y)
+        assert np.all(err <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * s) + 2.0 ** -17 * np.abs(y))
+
+
 # ----------------------------------------------------------------- the chain
 def test_norm_append_attention_as_a_layer_uses_them(csa):
     """Residual stream -> norm with 8-bit output (decoded as an 8-bit
