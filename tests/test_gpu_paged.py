@@ -629,6 +629,88 @@ def test_thousands_of_items_of_one_tile_and_of_none(csa):
         assert bool(torch.isneginf(lse[i:i + 256][~on]).all())
 
 
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("T,gain", [(130, 2.0), (900, 0.5)])
+def test_channels_far_larger_than_the_others(csa, T, gain, few):
+    """Channels of 20 times the others' size, whose weighted sums cancel: the
+    weights' rounding to fp16 shows there, within its bound."""
+    lens = [(5, T), (2, 40)]
+    B = Batch(420, _thin(lens, 64) if few else lens, 64, "fp8", 64, q_gain=gain)
+    rng = np.random.default_rng(5)
+    big = rng.choice(512, 16, replace=False)
+    for b, (_, n) in enumerate(lens):
+        x = rng.standard_normal((n, 512))
+        x[:, big] *= 20
+        _set_entries(B, b, x)
+    out, lse = _run(csa, B, B.device(csa))
+    _check(out, lse, B.want())
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_block_exponents_of_the_largest_entries(csa, few):
+    """Exponent bytes 143 to 151, past fp16's powers of two, with the codes that
+    stay under 65504 (a bit or four each: exact in fp16), beside bytes 103 and
+    on, and 0."""
+    B = Batch(421, _thin([(3, 200)], 16) if few else [(3, 200)], 16, "fp8", 16)
+    codes = np.array([c for c in range(256) if c & 0x7F != 0x7F])
+    size = np.abs(fp8_window_dequant_rows(np.concatenate([np.resize(codes, 512), np.full(16, 127)])[None].astype(np.uint8))[0, :len(codes)])
+    rng = np.random.default_rng(6)
+    for p in range(200):
+        row = B.pages[B.table[0, p // 16], p % 16]
+        row[512:] = np.where(rng.random(16) < 0.6, rng.integers(143, 152, 16), rng.integers(103, 143, 16))
+        row[512 + p % 16] = 0
+        for k in range(16):
+            few_bits = codes[size * 2.0 ** (int(row[512 + k]) - 127) < 65504]
+            row[32 * k:32 * k + 32] = rng.choice(few_bits, 32)
+    x = gather(B.pages, B.table, 0, range(200))[1]
+    assert 32768 <= np.abs(x).max() < 65504
+    out, lse = _run(csa, B, B.device(csa), scale=1e-6)
+    # byte 0 is 2^-127: below 448 * 2^-127, zero in fp16
+    want = B.want(scale=1e-6)
+    _check(out, lse, (want[0], want[1], want[2] + 2.0 ** -100, want[3], want[4]))
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_attention_without_lse(csa, H):
+    B = Batch(422, [(1, 700), (1, 0), (1, 33)], H, "fp8", 16)
+    kv = B.device(csa)
+    for sink in (None, torch.from_numpy(B.sink).cuda()):
+        outs = []
+        for lse in (None, torch.empty(3, H, device="cuda")):
+            out = torch.full((3, H, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+            csa.csa_paged_attn(csa.paged_attn_args(q=B.q.cuda(), kv=kv, out=out, lse=lse, softmax_scale=0.04, sink=sink))
+            outs.append(out)
+        torch.cuda.synchronize()
+        assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("few", [False, True])
+def test_a_query_out_of_range_spoils_its_own_row(csa, few):
+    """NaN, infinite and too large queries, and logits past fp32: no bit of the
+    other rows of their items changes."""
+    lens = [(6, 300), (2, 70)]
+    H = 16
+    B = Batch(423, _thin(lens, H) if few else lens, H, "fp8", 16)
+    B.pages[B.table[0, 0], 5, :512] = 0x7E                # an entry of 448 * 2^7 throughout
+    B.pages[B.table[0, 0], 5, 512:] = 134
+    kv = B.device(csa)
+    for scale in (0.04, 1e30):
+        first = _run(csa, B, kv, scale=scale)
+        assert bool(torch.isfinite(first[1]).all())
+        q, bad = B.q.cuda().clone(), [(0, 0), (1, 15), (4, 7), (7, 3)]
+        if scale == 0.04:
+            for (r, h), v in zip(bad, (float("nan"), float("inf"), -1e38, 1e30)):
+                q[r, h, 3 * h:3 * h + 40] = v
+        else:                                              # |<q, x>| about 22 * 6e4 * 57344: times 1e30 past fp32
+            for r, h in bad:
+                q[r, h] = 6e4 * torch.sign(q[r, h])
+        again = _run(csa, B, kv, scale=scale, q=q)
+        keep = torch.ones(B.rows, H, dtype=torch.bool, device="cuda")
+        for r, h in bad:
+            keep[r, h] = False
+        assert torch.equal(first[0][keep], again[0][keep]) and torch.equal(first[1][keep], again[1][keep])
+
+
 # -------------------------------------------------------------------- append
 def _append(csa, B, src, n_rows=None, **kw):
     kv = B.device(csa)
