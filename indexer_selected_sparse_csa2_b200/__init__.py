@@ -331,23 +331,24 @@ def csa_sparse_attn(args: AttnArgs, workspace=None, stream=None, device=None) ->
 
 
 def _cuda_device(args, where: str):
-    """Device of the tensors that ``args`` was built from (None: the fields were
-    set by hand).  A kernel must not get host pointers: tensors elsewhere than
-    on a CUDA device are refused here, before any launch."""
+    """Index of the device of the tensors that ``args`` was built from (None: the
+    fields were set by hand).  A kernel must not get host pointers: tensors
+    elsewhere than on a CUDA device are refused here, before any launch."""
     dev = getattr(args, "_device", None)
-    if dev is not None and dev.type != "cuda":
+    if dev is not None and dev.__class__ is not int:
         raise ValueError(f"{where}: tensors must be on a CUDA device, not on {dev}")
     return dev
 
 
 def _workspace_bytes(workspace, dev, where: str) -> int:
-    """Size of a workspace tensor; ``dev``: the device it has to be on (None: any
-    CUDA device).  A view with gaps or repeats spans other bytes than its
-    elements' sum."""
+    """Size of a workspace tensor; ``dev``: index of the device it has to be on
+    (None: any CUDA device).  A view with gaps or repeats spans other bytes than
+    its elements' sum."""
     if workspace is None:
         return 0
-    if not workspace.is_cuda or (dev is not None and workspace.device != dev):
-        raise ValueError(f"{where}: workspace is on {workspace.device}, not on {dev or 'a CUDA device'}")
+    at = workspace.get_device()                     # -1: the CPU
+    if at < 0 or (dev is not None and at != dev):
+        raise ValueError(f"{where}: workspace is on {workspace.device}, not on {'a CUDA device' if dev is None else f'cuda:{dev}'}")
     if not workspace.is_contiguous():
         raise ValueError(f"{where}: workspace must be contiguous")
     return workspace.numel() * workspace.element_size()
@@ -358,7 +359,7 @@ def _on_device(args, stream, call, where: str) -> None:
     be the current one; ``stream`` None = that device's current stream."""
     dev = _cuda_device(args, where)
     cuda = _torch().cuda
-    if dev is None or dev.index == cuda.current_device():
+    if dev is None or dev == cuda.current_device():
         _check(call(_stream(stream)), where)
         return
     with cuda.device(dev):
@@ -382,7 +383,7 @@ def csa_paged_attn(args: PagedAttnArgs, workspace=None, stream=None, device=None
     # the library checks a given workspace's size itself; query it only to allocate one
     if workspace is None:
         with _torch().cuda.stream(stream):          # its memory is the stream's: freed here, reused behind the call
-            workspace = _workspace(csa_paged_attn_workspace_size(args), device or dev or "cuda")
+            workspace = _workspace(csa_paged_attn_workspace_size(args), device or ("cuda" if dev is None else f"cuda:{dev}"))
     nbytes = _workspace_bytes(workspace, dev, "csa_paged_attn")
     _on_device(args, stream, lambda st: _paged_attn(args, _ptr(workspace), nbytes, st), "csa_paged_attn")
 
@@ -567,11 +568,13 @@ def _expect(t, dtype: str, what: str, shape=None, contiguous=False) -> None:
 
 
 def _device_of(*tensors):
-    """The device that all of the tensors are on."""
+    """Index of the CUDA device that all of the tensors are on, or the device
+    itself where it is no CUDA device (a call refuses such arguments)."""
     devs = {t.device for t in tensors if t is not None}
     if len(devs) != 1:
         raise ValueError(f"tensors on different devices: {sorted(map(str, devs))}")
-    return devs.pop()
+    dev = devs.pop()
+    return dev.index if dev.type == "cuda" else dev
 
 
 def _row_stride(t) -> int:

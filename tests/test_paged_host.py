@@ -268,10 +268,13 @@ def test_attention_refuses_workspaces_it_could_not_write(csa):
         csa.csa_paged_attn(kv, workspace=torch.zeros(need, dtype=torch.uint8))
 
     class Workspace:                                  # stands in for a tensor on a GPU
-        is_cuda, device = True, torch.device("cuda", 1)
+        device = torch.device("cuda", 1)
 
         def __init__(self, contiguous):
             self.is_contiguous = lambda: contiguous
+
+        def get_device(self):
+            return 1
 
         def numel(self):
             return need
@@ -279,10 +282,10 @@ def test_attention_refuses_workspaces_it_could_not_write(csa):
         def element_size(self):
             return 1
 
-    for dev in (None, torch.device("cuda", 1)):
+    for dev in (None, 1):
         assert csa._workspace_bytes(Workspace(True), dev, "call") == need
         with pytest.raises(ValueError, match="contiguous"):
             csa._workspace_bytes(Workspace(False), dev, "call")
     with pytest.raises(ValueError, match="cuda:0"):
-        csa._workspace_bytes(Workspace(True), torch.device("cuda", 0), "call")
+        csa._workspace_bytes(Workspace(True), 0, "call")
     assert csa._workspace_bytes(None, None, "call") == 0
