@@ -890,6 +890,78 @@ def test_append_of_thousands_of_rows(csa, fmt, dtype, case):
         assert np.all(err <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * s) + 2.0 ** -17 * np.abs(y))
 
 
+@pytest.mark.parametrize("H", [2, 72])
+def test_the_most_sequences_of_a_call(csa, H):
+    """65536 sequences of one entry each, half of them with a new token (H = 2)
+    or all (H = 72: the kernel for many rows), behind 7 rows of no sequence:
+    append writes every entry, attention gives it back."""
+    B, page = 65536, 3
+    rng = np.random.default_rng(32)
+    n = (rng.random(B) < 0.5).astype(np.int32) if H == 2 else np.ones(B, dtype=np.int32)
+    cu = torch.from_numpy((7 + np.concatenate([[0], np.cumsum(n)])).astype(np.int32)).cuda()
+    rows = int(cu[-1]) + 6
+    g = torch.Generator(device="cuda").manual_seed(32)
+    pages = torch.full((B + 1, page, 528), 0x7E, dtype=torch.uint8, device="cuda")
+    table = torch.randperm(B + 1, generator=g, device="cuda")[:B].to(torch.int32)[:, None].contiguous()
+    kv = csa.paged_kv(pages=pages, block_table=table, cu_q=cu, kv_len=torch.ones(B, dtype=torch.int32, device="cuda"))
+    src = torch.randn(rows, 512, generator=g, device="cuda").to(torch.bfloat16)
+    enc = torch.empty(rows, 528, dtype=torch.uint8, device="cuda")
+    csa.csa_quant_kv(src, csa.CSA_FMT_FP8_E4M3_UE8M0X32, enc)
+    csa.csa_paged_append(csa.paged_append_args(src=src, kv=kv))
+    on = torch.from_numpy(n).cuda().bool()
+    want = torch.full_like(pages, 0x7E)
+    want[table[on, 0].long(), 0] = enc[7:-6]
+    assert torch.equal(pages, want)
+    del want
+    q = torch.randn(rows, H, 512, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 3.0)
+    lse = torch.full((rows, H), 3.0, device="cuda")
+    csa.csa_paged_attn(csa.paged_attn_args(q=q, kv=kv, out=out, lse=lse, softmax_scale=0.04))
+    torch.cuda.synchronize()
+    x = enc[:, :512].contiguous().view(torch.float8_e4m3fn).float().view(rows, 16, 32)
+    x = (x * torch.exp2(enc[:, 512:].float() - 127)[:, :, None]).view(rows, 512)
+    for i in range(0, rows, 4096):
+        k = slice(max(i, 7), min(i + 4096, rows - 6))
+        o, xx = out[k].double(), x[k].double()[:, None]
+        assert bool(((o - xx).abs() <= (2.0 ** -8 + 2.0 ** -11) * xx.abs()).all())
+        z = q[k].double() * xx
+        l, size = 0.04 * z.sum(-1), 0.04 * z.abs().sum(-1)
+        assert bool(((lse[k].double() - l).abs() <= 2.0 ** -17 * size + 2.0 ** -18 * (1 + l.abs())).all())
+    for edge in (slice(0, 7), slice(rows - 6, rows)):
+        assert bool((out[edge] == 3.0).all()) and bool((lse[edge] == 3.0).all())
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_rows_before_the_first_sequence_stay(csa, H):
+    B = Batch(33, [(3, 50), (2, 20)], H, "fp8", 16, tail_rows=4)
+    kv = B.device(csa)
+    want = _run(csa, B, kv, sink=B.sink)
+    pages = _append(csa, B, torch.randn(B.rows, 512, generator=torch.Generator("cuda").manual_seed(1), device="cuda"))
+    B.device(csa)
+    B.d["cu_q"].add_(4)
+    kv = csa.paged_kv(**B.d)
+    q = torch.roll(B.q.cuda(), 4, 0)
+    out, lse = _run(csa, B, kv, sink=B.sink, q=q)
+    assert torch.equal(out[4:], want[0][:5]) and torch.equal(lse[4:], want[1][:5])
+    assert bool((out[:4] == 3.0).all()) and bool((lse[:4] == 3.0).all())
+    src = torch.roll(torch.randn(B.rows, 512, generator=torch.Generator("cuda").manual_seed(1), device="cuda"), 4, 0)
+    csa.csa_paged_append(csa.paged_append_args(src=src, kv=kv))
+    torch.cuda.synchronize()
+    assert np.array_equal(B.d["pages"].cpu().numpy(), pages)
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_the_largest_pages(csa, H):
+    B = Batch(34, [(2, 66000), (1, 65537), (1, 65536)], H, "fp4", 65536)
+    out, lse = _run(csa, B, B.device(csa), window=900)
+    kp = [gather(B.pages, B.table, b, range(T - 1000, T)) for b, (_, T) in enumerate(B.lens)]
+    q, r = B.q.double().numpy(), 0
+    for b, (n, T) in enumerate(B.lens):
+        w = attend(q[r:r + n], np.arange(T - n, T), *kp[b], 512 ** -0.5, 900)
+        _check(out[r:r + n], lse[r:r + n], w)
+        r += n
+
+
 # ----------------------------------------------------------------- the chain
 def test_norm_append_attention_as_a_layer_uses_them(csa):
     """Residual stream -> norm with 8-bit output (decoded as an 8-bit
