@@ -825,11 +825,13 @@ static bool pg_one(const csa_paged_attn_args* a) { return a->n_rows * a->H <= (i
 // Parts of the grid (pairs, or CTAs): all SMs, fewer when the call cannot have
 // two tiles for each.
 static int pg_parts(const csa_paged_attn_args* a) {
-  const int rows = pg_one(a) ? kPgRows / 2 : kPgRows, most = pg_one(a) ? kNumSMs : kNumSMs / 2;
+  const bool one = pg_one(a);
+  const int rows = one ? kPgRows / 2 : kPgRows, most = one ? kNumSMs : kNumSMs / 2;
   const int64_t items = (a->n_rows * a->H + rows - 1) / rows + a->kv.B;
-  const int e = pg_one(a) ? kPgTile<kPgRows / 2> : kPgTile<kPgRows>;
+  const int e = one ? kPgTile<kPgRows / 2> : kPgTile<kPgRows>;
   const int64_t tiles = ((int64_t)a->kv.max_pages * a->kv.page_size + e - 1) / e;
-  return items * (tiles + kPgItemCost) / 2 < most ? (int)((items * (tiles + kPgItemCost) + 1) / 2) : most;
+  const int64_t cost = items * (tiles + (one ? kPgItemCost<kPgRows / 2> : kPgItemCost<kPgRows>));
+  return cost / 2 < most ? (int)((cost + 1) / 2) : most;
 }
 static size_t pg_al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -839,7 +841,8 @@ static size_t pg_al256(size_t x) { return (x + 255) & ~(size_t)255; }
 static size_t pg_slots(const csa_paged_attn_args* a) {
   const int64_t items = (a->n_rows * a->H + 63) / 64 + a->kv.B;
   const int64_t tiles = ((int64_t)a->kv.max_pages * a->kv.page_size + 31) / 32;
-  return 2 * (size_t)(items * (tiles + kPgItemCost) < kNumSMs ? items * (tiles + kPgItemCost) : kNumSMs);
+  const int64_t cost = items * (tiles + kPgItemCost<64>);
+  return 2 * (size_t)(cost < kNumSMs ? cost : kNumSMs);
 }
 
 size_t paged_attn_ws_bytes(const csa_paged_attn_args* a) {

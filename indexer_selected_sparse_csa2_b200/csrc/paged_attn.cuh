@@ -45,9 +45,14 @@ constexpr uint32_t kPgSCol = 32 * kPgQTmemBlocks;   // S: 64 columns
 constexpr uint32_t kPgOCol = 256;
 constexpr uint32_t kPgTmemCols = 512;
 static_assert(kPgSCol + kPgE <= kPgOCol, "TMEM map");
-// An item's own cost (Q, output) in key tiles: 8 prompts of up to 2047 tokens
-// take 748, 678, 696 and 715 us with 2, 4, 6 and 8.
-constexpr int kPgItemCost = 4;
+// An item's own cost (Q, first tile, output) in key tiles, by its rows.  Pairs: 8
+// prompts of up to 2047 tokens take 748, 678, 696 and 715 us with 2, 4, 6 and 8.
+// One CTA, tiles half as long: 64 sequences' tokens, 64 heads each, behind 1 to
+// 8000 FP8 entries take 111, 102, 89, 81 and 79 us with 4, 6, 8, 12 and 16; 200
+// sequences' tokens, 16 heads each, behind 1 to 2000 FP4 entries 96, 81, 73, 65
+// and 67.  Batches of equal lengths take the same with each.
+template <int ROWS>
+constexpr int kPgItemCost = ROWS == 64 ? 12 : 4;
 constexpr float kPgRescale = 8.0f;        // lazy-rescale threshold (exp2 units)
 constexpr float kPgPExp = 6.0f;           // P carries a factor 2^6
 constexpr float kPgLog2e = 1.4426950408889634f;
@@ -201,14 +206,14 @@ struct PgWalk {
   CSA_DEV void item(const PgParams& p) {
     pg_item<ROWS>(p, s, j, k0, k1);
     total = pg_tiles<ROWS>(k0, k1);
-    off = min(max(at - kPgItemCost, 0), total);
-    take = (int)min((int64_t)total, max(at + left - kPgItemCost, (int64_t)0)) - off;
+    off = min(max(at - kPgItemCost<ROWS>, 0), total);
+    take = (int)min((int64_t)total, max(at + left - kPgItemCost<ROWS>, (int64_t)0)) - off;
   }
   // does this part do anything for the item? (a tileless one belongs to the
   // part at its start)
   CSA_DEV bool mine() const { return take > 0 || (total == 0 && at == 0); }
   CSA_DEV void step(const PgParams& p) {
-    left -= kPgItemCost + total - at;
+    left -= kPgItemCost<ROWS> + total - at;
     at = 0;
     if (left <= 0) return;
     if (++j >= s.tiles) {
@@ -281,7 +286,7 @@ CSA_DEV int64_t pg_group_cost(const PgParams& p, int g, int lane) {
     for (int j = 0; j < s.tiles; ++j) {
       int k0, k1;
       pg_item<ROWS>(p, s, j, k0, k1);
-      u += kPgItemCost + pg_tiles<ROWS>(k0, k1);
+      u += kPgItemCost<ROWS> + pg_tiles<ROWS>(k0, k1);
     }
   }
 #pragma unroll 1
@@ -297,7 +302,7 @@ CSA_DEV int64_t pg_group_cost(const PgParams& p, int g, int lane) {
     for (int j = lane; j < q.tiles; j += 32) {
       int k0, k1;
       pg_item<ROWS>(p, q, j, k0, k1);
-      v += kPgItemCost + pg_tiles<ROWS>(k0, k1);
+      v += kPgItemCost<ROWS> + pg_tiles<ROWS>(k0, k1);
     }
     v = pg_warp_sum64(v);
     if (lane == l) u = v;
@@ -372,7 +377,7 @@ CSA_DEV void pg_plan(const PgParams& p, int64_t* gsum, int64_t* start, int part,
         if (j + lane < s.tiles) {
           int k0, k1;
           pg_item<ROWS>(p, s, j + lane, k0, k1);
-          w = kPgItemCost + pg_tiles<ROWS>(k0, k1);
+          w = kPgItemCost<ROWS> + pg_tiles<ROWS>(k0, k1);
         }
         const int64_t sum = pg_warp_sum64(w);
         if (at < sum || j + 32 >= s.tiles) {
