@@ -269,8 +269,10 @@ csa_status csa_sparse_attn(const csa_attn_args* a, void* workspace, size_t works
  *                         are 0; code = E4M3_rne_sat(y * (1 / scale))
  * y enters the codes unrounded.  x, residual, residual_out and out share one
  * type; residual_out and out may be x or residual themselves (same pointer
- * and stride), any other overlap is outside the contract.  Non-finite inputs,
- * and a row of zeros with eps = 0, are outside the contract. */
+ * and stride), any other overlap is outside the contract.  So are non-finite
+ * inputs, rows whose sum of squares fp32 does not hold (values from 1.8e19 /
+ * sqrt(dim) on may pass it), and with eps = 0 rows of zeros or of values whose
+ * squares vanish in fp32. */
 typedef enum { CSA_SCALE_NONE = 0, CSA_SCALE_UE8M0X32 = 1, CSA_SCALE_F32X128 = 2 } csa_scale_kind;
 
 typedef struct {
@@ -329,7 +331,10 @@ typedef struct {
  * `rope_cs` (channels (448 + 2j, 449 + 2j) times e^{i angle j} of the row's
  * position), encoded as kv.fmt and written to its position's entry.  Without
  * norm and rope_cs the entries are bit for bit those of csa_quant_kv.  No two
- * rows of a call may share an entry. */
+ * rows of a call may share an entry.  csa_paged_attn reads these entries; the
+ * calls that read a contiguous cache (csa_index_topk, csa_sparse_attn,
+ * csa_layer_step) take no page table and would need a copy of them.  Rows that
+ * csa_rms_norm excludes are excluded from the norm here too. */
 typedef struct {
   csa_paged_kv kv;
   const void* src;           /* fp32 / bf16, row i at src + i * src_row_stride elements */
@@ -353,8 +358,13 @@ csa_status csa_paged_append(const csa_paged_append_args* a, csa_stream_t stream)
  * A row that sees no entry gets out = 0 and lse = sink_h (-inf without a
  * sink).  One new token per sequence is the decode step, kv_len[b] = n_b a
  * whole prompt, anything between a chunk; sequences of a call may differ.
- * Entries must decode to |x| < 65504 and queries hold |q| < 65504 (fp16
- * operands, fp32 accumulation); rotated queries are rounded to fp16.  An entry
+ * Entries must decode to |x| < 65504 and queries hold |q| < 65504: operands are
+ * fp16, sums fp32.  Within that an entry's value is exact from 2^-14 on, and
+ * below rounded to a multiple of 2^-24 (FP8 blocks of small exponents), and so
+ * is a query's; rotated queries are rounded to fp16 throughout, and so are the
+ * weights, to 2^-11 of each: an output is off by up to 2^-11 sum_e w_e |x_e|
+ * beside its own rounding.  (csa_sparse_attn holds weights and rotated queries
+ * in two fp16 parts and is closer where large values cancel.)  An entry
  * that does not (NaN codes, a scale past the range) may spoil any row of its
  * sequence in the call, also one whose mask leaves it out; entries that no row
  * of the call sees are not looked at, whatever their bytes.  A query that does
@@ -362,7 +372,10 @@ csa_status csa_paged_append(const csa_paged_append_args* a, csa_stream_t stream)
  * stay below 2.3e38 (fp32's largest value / log2 e), as it does with any such
  * operands up to softmax_scale = 1e26.
  * The workspace holds partial results from the call to its end: calls that may
- * run at the same time (two streams, two captured graphs) need one each. */
+ * run at the same time (two streams, two captured graphs) need one each.
+ * Which of two kernels runs follows n_rows * H against 64 * B, which the host
+ * knows: padding rows count there, and so do sequences without new tokens.  out
+ * and lse overlap no operand. */
 typedef struct {
   csa_paged_kv kv;
   const void* q;             /* bf16, row i head h at q + i*q_row_stride + h*q_head_stride elements */

@@ -33,9 +33,9 @@
 // softmax warpgroup left 96 registers a thread, and with shared memory at its
 // maximum a spilled register is a trip to L2.
 //
-// Measured: 4 x 512 new tokens x 64 heads behind up to 16384 FP8 entries 2.06
-// ms alone (1067 TFLOP/s), 2.30 ms back to back (956); 8 prompts of up to 2047
-// tokens x 32 heads 645 / 678 us (710 / 675 TFLOP/s); 4 x 1024 tokens, window
+// Measured: 4 x 512 new tokens x 64 heads behind up to 16384 FP8 entries 2.02
+// ms alone (1090 TFLOP/s), 2.28 ms back to back (963); 8 prompts of up to 2047
+// tokens x 32 heads 637 / 665 us (719 / 689 TFLOP/s); 4 x 1024 tokens, window
 // 128, 206 us (1.89 TB/s of queries, entries and output).  A tile of 128 x 64
 // takes about 2050 cycles: the tensor pipe is busy for half of them, shared
 // memory for two thirds, instruction issue for 56 %.
@@ -820,7 +820,11 @@ __global__ void __launch_bounds__(128 * kPgCombRows) paged_attn_combine_kernel(c
 // Pairs and single CTAs, back to back: 8 x 1 token x 64 heads behind up to
 // 65536 FP8 entries 119 and 94 us; 32 x 1 token x 16 heads, FP4, 106 and 70 us;
 // 16 x 1 token x 128 heads 117 and 144 us; 4 x 512 tokens x 64 heads 2.30 and
-// 3.42 ms.
+// 3.42 ms.  64 tokens x 64 heads behind 8000 entries beside a chunk of 512 tokens
+// behind as many: 745 and 917 us, the two parts alone 126 + 608.  It is an
+// average over what the host knows: 64 tokens of which two are one sequence's
+// take 165 us on the pairs that they then get, 129 on single CTAs; that chunk,
+// padded with 600 sequences without tokens, 800 us on single CTAs, 609 on pairs.
 static bool pg_one(const csa_paged_attn_args* a) { return a->n_rows * a->H <= (int64_t)kPgRows / 2 * a->kv.B; }
 // Parts of the grid (pairs, or CTAs): all SMs, fewer when the call cannot have
 // two tiles for each.

@@ -13,15 +13,17 @@
 // S and the MN-major A operand of O^T, where the pair kernel's CTAs keep two
 // tiles and decode half of the other's channels as well.
 //
-// Bound: the tensor pipe and shared memory alike, about 1200 cycles a tile (S
-// 24 x 16 + 8 x 40, O^T 8 x 48; 36 KB written, 112 KB read); it takes 1250.
-// Five tiles are in flight, because a tile's way (decode, S, softmax, PV) is
-// five times as long; with tiles of 64 entries, two and a half of them, 64
-// entries took 3600 cycles.
-// Measured: 8 x 1 token x 64 heads behind up to 65536 FP8 entries 94 us (2.0
-// TB/s of entries, 500 TFLOP/s), of which 15 us are the first tile's way, the
-// last output and the combine; 32 x 1 token x 16 heads behind up to 16384 FP4
-// entries 70 us; one token behind 1000 entries 17.5 us.
+// Bound: latency.  A tile takes 0.93 us (FP8, 64 heads; by the growth of the time
+// with the length, 8 tokens behind 65536 and 131072 entries), 1700 to 1800 cycles,
+// of which the tensor pipe needs 1090 (S 24 x 16 + 8 x 40, O^T 8 x 48) and shared
+// memory 1190 (36 KB written, 112 KB read): with five tiles in flight, a tile's
+// way (loads, decode, S, softmax, PV) is five times that long.  FP4 entries, with
+// fewer bytes to load, take 0.88 us; 16 heads 0.82 and 0.79.  With tiles of 64
+// entries, two and a half of them in flight, 64 entries took 3600 cycles.
+// Measured: 8 x 1 token x 64 heads behind up to 65536 FP8 entries 92 us (2.1
+// TB/s of entries, 520 TFLOP/s): 72 us of tiles, and 20 us of launches, plan, first
+// tile, output and combine; 32 x 1 token x 16 heads behind up to 16384 FP4
+// entries 70 us; one token behind 1000 entries 17 us.
 #include "paged_attn.cuh"
 
 namespace csa {
