@@ -385,7 +385,7 @@ typedef struct {
   int32_t H, D;              /* H in 1..128; D must be 512 */
   float softmax_scale;       /* 0..1e30 */
   int32_t window;            /* 0: no window; else >= 1 */
-  const float* sink;         /* optional fp32 [H] sink logits */
+  const float* sink;         /* optional fp32 [H] sink logits: -inf, or as l_e */
   const float* rope_cs;      /* optional fp32 [n_rows][32][2]: q rotated forward, out back */
   void* out;                 /* bf16 [n_rows][H][512], contiguous */
   float* lse;                /* optional fp32 [n_rows][H] (natural log) */
