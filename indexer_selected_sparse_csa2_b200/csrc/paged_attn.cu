@@ -35,7 +35,7 @@
 //
 // Measured: 4 x 512 new tokens x 64 heads behind up to 16384 FP8 entries 2.02
 // ms alone (1090 TFLOP/s), 2.28 ms back to back (963); 8 prompts of up to 2047
-// tokens x 32 heads 637 / 665 us (719 / 689 TFLOP/s); 4 x 1024 tokens, window
+// tokens x 32 heads 637 / 678 us (719 / 675 TFLOP/s); 4 x 1024 tokens, window
 // 128, 206 us (1.89 TB/s of queries, entries and output).  A tile of 128 x 64
 // takes about 2050 cycles: the tensor pipe is busy for half of them, shared
 // memory for two thirds, instruction issue for 56 %.

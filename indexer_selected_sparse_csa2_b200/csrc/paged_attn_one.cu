@@ -20,8 +20,8 @@
 // way (loads, decode, S, softmax, PV) is five times that long.  FP4 entries, with
 // fewer bytes to load, take 0.88 us; 16 heads 0.82 and 0.79.  With tiles of 64
 // entries, two and a half of them in flight, 64 entries took 3600 cycles.
-// Measured: 8 x 1 token x 64 heads behind up to 65536 FP8 entries 92 us (2.1
-// TB/s of entries, 520 TFLOP/s): 72 us of tiles, and 20 us of launches, plan, first
+// Measured: 8 x 1 token x 64 heads behind up to 65536 FP8 entries 93 us (2.1
+// TB/s of entries, 510 TFLOP/s): 72 us of tiles, and 20 us of launches, plan, first
 // tile, output and combine; 32 x 1 token x 16 heads behind up to 16384 FP4
 // entries 70 us; one token behind 1000 entries 17 us.
 #include "paged_attn.cuh"
